@@ -374,6 +374,108 @@ int moe_router_backward(const moe_bf16* x, int T, int H, const moe_bf16* w_r, in
                         size_t ws_bytes, moe_stream stream);
 
 /*
+ * Block-scaled storage: what an expert keeps between two uses, in OCP
+ * microscaling blocks of 32 values that share one power-of-two scale byte s
+ * (s = 255: the block held a NaN or an infinity and stands for 32 NaN).
+ *
+ * 8 bits, rows of activations (blocks along the row).  With m the block's
+ * largest magnitude:
+ *   s = max(biased exponent of m, 7)
+ *   q = clamp(rint(x * 2^(133-s)), -127, 127)       (nearest even)
+ *   value = q * 2^(s-133), a bf16;  |value - x| <= 2^(s-134) <= m/128
+ *   q int8 [rows, cols], scale uint8 [rows, cols/32].
+ *
+ * 4 bits, weights [E][Kd][N] (blocks along the contraction Kd):
+ *   s = max(biased exponent of m - 2, 2)
+ *   value = c * 2^(s-127), a bf16, with c the nearest (ties to the even code,
+ *   saturating) of +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}; code 0..7, plus 8 if negative.
+ * Packing values that a 4-bit block holds already changes none of them.  The
+ * codes are stored in the matrix instruction's operand order, in tiles of 16
+ * columns x 128 contraction values, KT = ceil(Kd/128) (codes behind Kd are 0):
+ *   q4 uint8 [E][N/16][KT][64][16]: byte [e][n/16][kt][16*g + n%16][4*t + i]
+ *      holds contraction index k = 128*kt + 32*g + 8*t + 2*i in its low four
+ *      bits and k + 1 in its high four;
+ *   s4 uint8 [E][N/16][KT][64]: the scale of block g at [16*g + n%16].
+ */
+
+/*
+ * Rows of activations to 8-bit blocks and back.
+ *   x bf16 [rows, cols];  q int8 [rows, cols];  scale uint8 [rows, cols/32].
+ *   offsets int32 [e_local+1] (device) or NULL: with it only the routed rows,
+ *   the first min(rows, offsets[e_local]), are read and written; the rows
+ *   behind them are left as they are.
+ * cols a multiple of 64 (MOE_ESHAPE), 0 <= rows < 2^31, e_local <= 512.
+ */
+int moe_pack8(const moe_bf16* x, int64_t rows, int cols, const int32_t* offsets, int e_local, int8_t* q,
+              uint8_t* scale, moe_stream stream);
+int moe_unpack8(const int8_t* q, const uint8_t* scale, int64_t rows, int cols, const int32_t* offsets, int e_local,
+                moe_bf16* x, moe_stream stream);
+
+/*
+ * moe_grouped_gemm_swiglu that saves (a, b) for the backward in 8-bit blocks,
+ * 2F*(1 + 1/32) bytes a row instead of 4F.  h is bit-identical to
+ * moe_grouped_gemm_swiglu's, and (ab8, ab8_scale) to moe_pack8 of the ab_save
+ * that call would have written; neither ab_save nor a second pass is needed.
+ *   ab8 int8 [cap_rows,2F];  ab8_scale uint8 [cap_rows,2F/32];  other arguments
+ *   as moe_grouped_gemm_swiglu.
+ * With the backward below, h need not be kept either: it recomputes h.
+ */
+int moe_grouped_gemm_swiglu_save8(const moe_bf16* x_perm, const moe_bf16* w_gate, const moe_bf16* w_up,
+                                  const int32_t* offsets, int e_local, int H, int F, int cap_rows, moe_bf16* h,
+                                  int8_t* ab8, uint8_t* ab8_scale, moe_stream stream);
+
+/* The same on the tokens through src (zero-copy dispatch): x, T, src, K and
+ * their errors as moe_grouped_gemm_swiglu_gather. */
+int moe_grouped_gemm_swiglu_gather_save8(const moe_bf16* x, int T, const int32_t* src, int K,
+                                         const moe_bf16* w_gate, const moe_bf16* w_up, const int32_t* offsets,
+                                         int e_local, int H, int F, int cap_rows, moe_bf16* h, int8_t* ab8,
+                                         uint8_t* ab8_scale, moe_stream stream);
+
+/*
+ * Down dgrad with the SwiGLU backward from the 8-bit (a, b).  For rows r of
+ * expert j, with a, b the values that (ab8, ab8_scale)[r] stand for:
+ *   dh = dy_perm[r] . w_down[j]^T   (fp32 accumulate),  s = sigmoid(a)
+ *   dab[r] = [bf16(dh*b*s*(1 + a*(1-s))) | bf16(dh*a*s)]
+ *   h[r]   = bf16(a*s*b)            (h NULL: not written), for moe_wgrad
+ * dab and h are the derivative and the value of the SwiGLU of the saved (a, b).
+ *   dy_perm bf16 [cap_rows,H];  w_down bf16 [e_local,F,H];  dab bf16 [cap_rows,2F];
+ *   h bf16 [cap_rows,F] or NULL.
+ */
+int moe_grouped_gemm_swiglu_bwd8(const moe_bf16* dy_perm, const moe_bf16* w_down, const int32_t* offsets,
+                                 int e_local, int H, int F, int cap_rows, const int8_t* ab8,
+                                 const uint8_t* ab8_scale, moe_bf16* dab, moe_bf16* h, moe_stream stream);
+
+/*
+ * Expert weights to 4-bit blocks (once, when a model is loaded) and back to
+ * the bf16 values they stand for (exactly).
+ *   w bf16 [E,Kd,N];  q4, s4 as above.  E <= 512; Kd, N multiples of 64
+ *   (MOE_ESHAPE); Kd*N*2 < 2^31.
+ */
+int moe_pack4(const moe_bf16* w, int E, int Kd, int N, uint8_t* q4, uint8_t* s4, moe_stream stream);
+int moe_unpack4(const uint8_t* q4, const uint8_t* s4, int E, int Kd, int N, moe_bf16* w, moe_stream stream);
+
+/*
+ * Gate/up and down products on 4-bit weights, for the few rows per expert of
+ * a decode step (one token to some hundreds): every weight byte of an expert
+ * with rows is read once per 16 to 64 of them.  Rows, offsets and results as
+ * in the bf16 products, with the packed weights' values for w:
+ *   h[r] = bf16(silu(x_r . w_gate[j]) * (x_r . w_up[j])),   c[r] = bf16(a[r] . w[j])
+ * with x_r = x[src[r] / K], or x[r] if src is NULL (x then has cap_rows rows in
+ * expert order; T and K are not used).  fp32 sums in one fixed order.
+ *   x bf16 [T,H];  gate, up packed from [e_local,H,F];  h bf16 [cap_rows,F];
+ *   a bf16 [cap_rows,Kd];  q4, s4 packed from [e_local,Kd,N];  c bf16 [cap_rows,N].
+ * A src value outside [0, T*K) reads a zero row.  Errors as
+ * moe_grouped_gemm_swiglu_gather (x at most 0xF0000000 bytes, cap_rows <= T*K,
+ * one expert's matrix below 2^30 values).
+ */
+int moe_grouped_gemm4_swiglu(const moe_bf16* x, int T, const int32_t* src, int K, const uint8_t* gate_q4,
+                             const uint8_t* gate_s4, const uint8_t* up_q4, const uint8_t* up_s4,
+                             const int32_t* offsets, int e_local, int H, int F, int cap_rows, moe_bf16* h,
+                             moe_stream stream);
+int moe_grouped_gemm4(const moe_bf16* a, const uint8_t* q4, const uint8_t* s4, const int32_t* offsets, int e_local,
+                      int Kd, int N, int cap_rows, moe_bf16* c, moe_stream stream);
+
+/*
  * Measurement aid, not a step of the layer: the bf16 MFMA rate this GPU
  * sustains.  Each of the blocks x 4 waves keeps its own 8 fragments of
  * operands in registers and runs iters rounds of a 4 x 4 block of

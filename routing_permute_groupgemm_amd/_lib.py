@@ -42,6 +42,15 @@ SIGNATURES = {
     "moe_router_workspace_size": ([_i, _i, _i], _z),
     "moe_router_logits": ([_p, _i, _i, _p, _i, _p, _p, _p, _z, _p], _i),
     "moe_router_backward": ([_p, _i, _i, _p, _i, _p, _p, _p, _p, _z, _p], _i),
+    "moe_pack8": ([_p, _i64, _i, _p, _i, _p, _p, _p], _i),
+    "moe_unpack8": ([_p, _p, _i64, _i, _p, _i, _p, _p], _i),
+    "moe_grouped_gemm_swiglu_save8": ([_p, _p, _p, _p, _i, _i, _i, _i, _p, _p, _p, _p], _i),
+    "moe_grouped_gemm_swiglu_gather_save8": ([_p, _i, _p, _i, _p, _p, _p, _i, _i, _i, _i, _p, _p, _p, _p], _i),
+    "moe_grouped_gemm_swiglu_bwd8": ([_p, _p, _p, _i, _i, _i, _i, _p, _p, _p, _p, _p], _i),
+    "moe_pack4": ([_p, _i, _i, _i, _p, _p, _p], _i),
+    "moe_unpack4": ([_p, _p, _i, _i, _i, _p, _p], _i),
+    "moe_grouped_gemm4_swiglu": ([_p, _i, _p, _i, _p, _p, _p, _p, _p, _i, _i, _i, _i, _p, _p], _i),
+    "moe_grouped_gemm4": ([_p, _p, _p, _p, _i, _i, _i, _i, _p, _p], _i),
     "moe_probe_mfma": ([_p, _i, _i, _p, _p], _i),
     "moe_probe_mfma16": ([_p, _i, _i, _p, _p], _i),
     "moe_probe_copy": ([_p, _p, _i64, _i, _i, _p], _i),
@@ -512,6 +521,225 @@ def moe_router_backward(x, w_r, dlogits, dx=None, dw_r=None, ws=None, stream=Non
     _check(load().moe_router_backward(_ptr(x), T, H, _ptr(w_r), E, _ptr(dlogits), _ptr(dx), _ptr(dw_r), _ptr(ws),
                                       ws.numel(), _stream(stream)))
     return dx, dw_r
+
+
+def _routed(offsets):
+    """offsets or None -> its expert count (0 without)."""
+    if offsets is None:
+        return 0
+    _need(offsets, torch.int32, "offsets")
+    if offsets.dim() != 1 or offsets.numel() < 1:
+        raise MoeError(f"offsets: expected e_local + 1 entries, got {tuple(offsets.shape)}")
+    return offsets.numel() - 1
+
+
+def _save8(q, scale, rows, cols, dev, names=("q", "scale")):
+    """The caller's 8-bit buffers (checked: at least `rows` rows) or new ones."""
+    if q is None:
+        q = torch.empty((rows, cols), dtype=torch.int8, device=dev)
+    if scale is None:
+        scale = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
+    _need(q, torch.int8, names[0])
+    _need(scale, torch.uint8, names[1])
+    _rows(q, rows, cols, names[0])
+    _rows(scale, rows, cols // 32, names[1])
+    return q, scale
+
+
+def moe_pack8(x, q=None, scale=None, offsets=None, stream=None):
+    """Rows of bf16 -> (q int8 [rows, cols], scale uint8 [rows, cols/32]) in blocks of 32 columns.
+    offsets (int32 [e_local+1]): only the first offsets[e_local] rows are read and written."""
+    _need(x, torch.bfloat16, "x")
+    if x.dim() != 2:
+        raise MoeError(f"x: expected [rows, cols], got {tuple(x.shape)}")
+    rows, cols = x.shape
+    q, scale = _save8(q, scale, rows, cols, x.device)
+    _check(load().moe_pack8(_ptr(x), rows, cols, _ptr(offsets), _routed(offsets), _ptr(q), _ptr(scale),
+                            _stream(stream)))
+    return q, scale
+
+
+def moe_unpack8(q, scale, x=None, offsets=None, stream=None):
+    """The bf16 rows that (q, scale) stand for (rows and offsets as moe_pack8)."""
+    _need(q, torch.int8, "q")
+    _need(scale, torch.uint8, "scale")
+    if q.dim() != 2:
+        raise MoeError(f"q: expected [rows, cols], got {tuple(q.shape)}")
+    rows, cols = q.shape
+    _rows(scale, rows, cols // 32, "scale")
+    if x is None:
+        x = torch.empty((rows, cols), dtype=torch.bfloat16, device=q.device)
+    _need(x, torch.bfloat16, "x")
+    _rows(x, rows, cols, "x")
+    _check(load().moe_unpack8(_ptr(q), _ptr(scale), rows, cols, _ptr(offsets), _routed(offsets), _ptr(x),
+                              _stream(stream)))
+    return x
+
+
+def moe_grouped_gemm_swiglu_save8(x_perm, w_gate, w_up, offsets, cap_rows, h=None, ab8=None, ab8_scale=None,
+                                  stream=None):
+    """moe_grouped_gemm_swiglu with (a, b) saved in 8-bit blocks -> (h, ab8, ab8_scale)."""
+    _need(x_perm, torch.bfloat16, "x_perm")
+    _need(w_gate, torch.bfloat16, "w_gate")
+    _need(w_up, torch.bfloat16, "w_up")
+    _need(offsets, torch.int32, "offsets")
+    EL, H, F = w_gate.shape
+    if h is None:
+        h = torch.empty((max(cap_rows, 1), F), dtype=torch.bfloat16, device=x_perm.device)
+    _gate_up_checks(w_gate, w_up, offsets, cap_rows, h, None)
+    ab8, ab8_scale = _save8(ab8, ab8_scale, max(cap_rows, 0), 2 * F, x_perm.device, ("ab8", "ab8_scale"))
+    _rows(x_perm, cap_rows, H, "x_perm")
+    _check(load().moe_grouped_gemm_swiglu_save8(_ptr(x_perm), _ptr(w_gate), _ptr(w_up), _ptr(offsets), EL, H, F,
+                                                cap_rows, _ptr(h), _ptr(ab8), _ptr(ab8_scale), _stream(stream)))
+    return h, ab8, ab8_scale
+
+
+def moe_grouped_gemm_swiglu_gather_save8(x, src, K, w_gate, w_up, offsets, cap_rows, h=None, ab8=None,
+                                         ab8_scale=None, stream=None):
+    """The same, reading row r of the expert-grouped order from x[src[r] // K] (no x_perm)."""
+    _need(x, torch.bfloat16, "x")
+    _need(src, torch.int32, "src")
+    _need(w_gate, torch.bfloat16, "w_gate")
+    _need(w_up, torch.bfloat16, "w_up")
+    _need(offsets, torch.int32, "offsets")
+    EL, H, F = w_gate.shape
+    T = x.shape[0]
+    if h is None:
+        h = torch.empty((max(cap_rows, 1), F), dtype=torch.bfloat16, device=x.device)
+    _gate_up_checks(w_gate, w_up, offsets, cap_rows, h, None)
+    ab8, ab8_scale = _save8(ab8, ab8_scale, max(cap_rows, 0), 2 * F, x.device, ("ab8", "ab8_scale"))
+    _shape(x, (T, H), "x")
+    if src.numel() < cap_rows:
+        raise MoeError(f"src: expected at least {cap_rows} entries, got {src.numel()}")
+    _check(load().moe_grouped_gemm_swiglu_gather_save8(_ptr(x), T, _ptr(src), int(K), _ptr(w_gate), _ptr(w_up),
+                                                       _ptr(offsets), EL, H, F, cap_rows, _ptr(h), _ptr(ab8),
+                                                       _ptr(ab8_scale), _stream(stream)))
+    return h, ab8, ab8_scale
+
+
+def moe_grouped_gemm_swiglu_bwd8(dy_perm, w_down, offsets, cap_rows, ab8, ab8_scale, dab=None, h=None,
+                                 want_h=True, stream=None):
+    """Down dgrad and SwiGLU backward from the 8-bit (a, b) -> (dab, h); want_h=False: h is not recomputed."""
+    _need(dy_perm, torch.bfloat16, "dy_perm")
+    _need(w_down, torch.bfloat16, "w_down")
+    _need(offsets, torch.int32, "offsets")
+    EL, F, H = w_down.shape
+    if offsets.numel() < EL + 1:
+        raise MoeError(f"offsets: expected {EL + 1} entries, got {offsets.numel()}")
+    _rows(dy_perm, cap_rows, H, "dy_perm")
+    for t, dt, cols, name in ((ab8, torch.int8, 2 * F, "ab8"), (ab8_scale, torch.uint8, 2 * F // 32, "ab8_scale")):
+        _need(t, dt, name)
+        _rows(t, cap_rows, cols, name)
+    if dab is None:
+        dab = torch.empty((max(cap_rows, 1), 2 * F), dtype=torch.bfloat16, device=dy_perm.device)
+    if h is None and want_h:
+        h = torch.empty((max(cap_rows, 1), F), dtype=torch.bfloat16, device=dy_perm.device)
+    if not want_h:
+        h = None
+    _need(dab, torch.bfloat16, "dab")
+    _rows(dab, cap_rows, 2 * F, "dab")
+    if h is not None:
+        _need(h, torch.bfloat16, "h")
+        _rows(h, cap_rows, F, "h")
+    _check(load().moe_grouped_gemm_swiglu_bwd8(_ptr(dy_perm), _ptr(w_down), _ptr(offsets), EL, H, F, cap_rows,
+                                               _ptr(ab8), _ptr(ab8_scale), _ptr(dab), _ptr(h), _stream(stream)))
+    return dab, h
+
+
+def pack4_shapes(E, Kd, N):
+    """Shapes of (q4, s4) for weights [E, Kd, N]."""
+    KT = -(-Kd // 128)
+    return (E, N // 16, KT, 64, 16), (E, N // 16, KT, 64)
+
+
+def _weights4(w, Kd, name, E=None, N=None):
+    """Checks a (q4, s4) pair against the contraction length -> (q4, s4, E, N)."""
+    q4, s4 = w
+    _need(q4, torch.uint8, name + " q4")
+    _need(s4, torch.uint8, name + " s4")
+    if q4.dim() != 5:
+        raise MoeError(f"{name} q4: expected {len(pack4_shapes(1, 64, 64)[0])} dimensions, got {tuple(q4.shape)}")
+    E = q4.shape[0] if E is None else E
+    N = q4.shape[1] * 16 if N is None else N
+    shapes = pack4_shapes(E, Kd, N)
+    _shape(q4, shapes[0], name + " q4")
+    _shape(s4, shapes[1], name + " s4")
+    return q4, s4, E, N
+
+
+def moe_pack4(w, q4=None, s4=None, stream=None):
+    """Weights bf16 [E, Kd, N] -> (q4, s4) in 4-bit blocks of 32 along Kd (layout in moe.h)."""
+    _need(w, torch.bfloat16, "w")
+    if w.dim() != 3:
+        raise MoeError(f"w: expected [E, Kd, N], got {tuple(w.shape)}")
+    E, Kd, N = w.shape
+    if Kd % 64 or N % 64:
+        raise MoeError(f"w: Kd and N must be multiples of 64, got {tuple(w.shape)}")
+    shapes = pack4_shapes(E, Kd, N)
+    if q4 is None:
+        q4 = torch.empty(shapes[0], dtype=torch.uint8, device=w.device)
+    if s4 is None:
+        s4 = torch.empty(shapes[1], dtype=torch.uint8, device=w.device)
+    _weights4((q4, s4), Kd, "w", E, N)
+    _check(load().moe_pack4(_ptr(w), E, Kd, N, _ptr(q4), _ptr(s4), _stream(stream)))
+    return q4, s4
+
+
+def moe_unpack4(q4, s4, Kd, w=None, stream=None):
+    """The bf16 weights [E, Kd, N] that (q4, s4) stand for."""
+    q4, s4, E, N = _weights4((q4, s4), Kd, "w")
+    if w is None:
+        w = torch.empty((E, Kd, N), dtype=torch.bfloat16, device=q4.device)
+    _need(w, torch.bfloat16, "w")
+    _shape(w, (E, Kd, N), "w")
+    _check(load().moe_unpack4(_ptr(q4), _ptr(s4), E, Kd, N, _ptr(w), _stream(stream)))
+    return w
+
+
+def moe_grouped_gemm4_swiglu(x, src, K, gate, up, offsets, cap_rows, h=None, stream=None):
+    """Gate/up product and SwiGLU on 4-bit weights (gate, up: (q4, s4) pairs), row r from x[src[r] // K], or
+    from x[r] if src is None (rows already in expert order; K unused)."""
+    _need(x, torch.bfloat16, "x")
+    _need(offsets, torch.int32, "offsets")
+    if x.dim() != 2:
+        raise MoeError(f"x: expected [T, H], got {tuple(x.shape)}")
+    T, H = x.shape
+    gq, gs, EL, F = _weights4(gate, H, "gate")
+    uq, us, _, _ = _weights4(up, H, "up", EL, F)
+    if offsets.numel() < EL + 1:
+        raise MoeError(f"offsets: expected {EL + 1} entries, got {offsets.numel()}")
+    if src is None:
+        _rows(x, cap_rows, H, "x")
+    else:
+        _need(src, torch.int32, "src")
+        if src.numel() < cap_rows:
+            raise MoeError(f"src: expected at least {cap_rows} entries, got {src.numel()}")
+    if h is None:
+        h = torch.empty((max(cap_rows, 1), F), dtype=torch.bfloat16, device=x.device)
+    _need(h, torch.bfloat16, "h")
+    _rows(h, cap_rows, F, "h")
+    _check(load().moe_grouped_gemm4_swiglu(_ptr(x), T, _ptr(src), int(K or 0), _ptr(gq), _ptr(gs), _ptr(uq),
+                                           _ptr(us), _ptr(offsets), EL, H, F, cap_rows, _ptr(h), _stream(stream)))
+    return h
+
+
+def moe_grouped_gemm4(a, w, offsets, cap_rows, c=None, stream=None):
+    """c[r] = a[r] . w_j on 4-bit weights w = (q4, s4); rows in expert order."""
+    _need(a, torch.bfloat16, "a")
+    _need(offsets, torch.int32, "offsets")
+    if a.dim() != 2 or a.shape[0] < cap_rows:
+        raise MoeError(f"a: expected at least {cap_rows} rows, got {tuple(a.shape)}")
+    Kd = a.shape[1]
+    q4, s4, EL, N = _weights4(w, Kd, "w")
+    if offsets.numel() < EL + 1:
+        raise MoeError(f"offsets: expected {EL + 1} entries, got {offsets.numel()}")
+    if c is None:
+        c = torch.empty((max(cap_rows, 1), N), dtype=torch.bfloat16, device=a.device)
+    _need(c, torch.bfloat16, "c")
+    _rows(c, cap_rows, N, "c")
+    _check(load().moe_grouped_gemm4(_ptr(a), _ptr(q4), _ptr(s4), _ptr(offsets), EL, Kd, N, cap_rows, _ptr(c),
+                                    _stream(stream)))
+    return c
 
 
 def moe_probe_mfma(operands, iters, out=None, stream=None):

@@ -49,6 +49,7 @@
 #include <type_traits>
 
 #include "moe_common.hpp"
+#include "mx.hpp"
 
 namespace moe {
 
@@ -70,7 +71,17 @@ constexpr int kLdsBudget = 128 * 1024;  // LDS per workgroup for the stage ring
 #endif
 
 enum : int { LAY_KC = 0, LAY_MN = 1 };
-enum : int { EPI_BF16 = 0, EPI_SWIGLU = 1, EPI_SWIGLU_BWD = 2, EPI_F32 = 3 };
+// EPI_SWIGLU8 and EPI_SWIGLU_BWD8: the SwiGLU epilogues that write and read the
+// saved (a, b) in 8-bit blocks (mx.hpp)
+enum : int {
+    EPI_BF16 = 0,
+    EPI_SWIGLU = 1,
+    EPI_SWIGLU_BWD = 2,
+    EPI_F32 = 3,
+    EPI_SWIGLU8 = 4,
+    EPI_SWIGLU_BWD8 = 5
+};
+constexpr bool is_up(int epi) { return epi == EPI_SWIGLU || epi == EPI_SWIGLU8; }
 enum : int { SCHED_ROWS = 0, SCHED_WGRAD = 1 };
 
 struct GemmParams {
@@ -112,6 +123,8 @@ struct GemmParams {
     const float* bias;    // ROWS EPI_F32: added to every row, [N]
     int stagger_ticks;    // start delay step of the workgroups (100 MHz ticks; 0: none)
     int stagger_phases;
+    int8_t* q8;           // SWIGLU8 (out), SWIGLU_BWD8 (in): saved [a | b] in 8 bits, [rows, 2N]
+    uint8_t* s8;          // their scale bytes, [rows, 2N/32]
 };
 
 typedef __attribute__((ext_vector_type(4))) int i32x4;
@@ -305,7 +318,7 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
     using LY = Lay<BK>;
     constexpr int MTW = TL::kMTW, NTW = TL::kNTW, LPW = TL::kLoadsPerWave, S = TL::kStages, KK = TL::kKK;
     constexpr int LA = TL::kALoads / TL::kWaves;  // A loads per wave and stage
-    static_assert(!GATHER || (SCHED == SCHED_ROWS && EPI == EPI_SWIGLU) || (SCHED == SCHED_WGRAD && EPI == EPI_F32),
+    static_assert(!GATHER || (SCHED == SCHED_ROWS && is_up(EPI)) || (SCHED == SCHED_WGRAD && EPI == EPI_F32),
                   "gathered A rows: the gate/up GEMM and the weight gradient");
     // gathered rows of the weight gradient's contraction (GATHER with SCHED_WGRAD)
     constexpr bool kGW = GATHER && SCHED == SCHED_WGRAD;
@@ -324,7 +337,8 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
     // (MOE_GEMM_MFMA16_WGRAD=1: MN-layout A fragments, and each lane stores its
     // 16 bytes of fp32 dW straight from the accumulators); it ran 5% slower
     // than its 32x32x16 body, whose staged epilogue stores whole lines.
-    constexpr bool kMf16 = ((MOE_GEMM_MFMA16 && EPI == EPI_SWIGLU_BWD && SCHED == SCHED_ROWS) ||
+    constexpr bool kMf16 = ((MOE_GEMM_MFMA16 && (EPI == EPI_SWIGLU_BWD || EPI == EPI_SWIGLU_BWD8) &&
+                             SCHED == SCHED_ROWS) ||
                             (MOE_GEMM_MFMA16_WGRAD && EPI == EPI_F32 && SCHED == SCHED_WGRAD)) &&
                            BM == 256 && BN == 256 && WM == 2 && WN == 2 && BK == 32;
     constexpr int MB16 = kMf16 ? BM / WM / 16 : 1;  // 16-row blocks per wave
@@ -345,7 +359,7 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
     int tiles_n;  // tiles along N (ROWS) ; tiles per group (WGRAD)
     int tiles_mw = 0;
     if (SCHED == SCHED_ROWS) {
-        tiles_n = EPI == EPI_SWIGLU ? (p.N + BN / 2 - 1) / (BN / 2) : (p.N + BN - 1) / BN;
+        tiles_n = is_up(EPI) ? (p.N + BN / 2 - 1) / (BN / 2) : (p.N + BN - 1) / BN;
         // exclusive scan of per-expert m-tile counts; each thread owns a run of experts
         constexpr int PER = (kMaxGroups + TL::kThreads - 1) / TL::kThreads;
         const int j0 = tid * PER;
@@ -418,7 +432,7 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
         return (SCHED == SCHED_ROWS && BM < 256) ? (mt * WM + wm) * 32 : wm * (BM / WM) + mt * 32;
     };
     auto col_of = [&](int nt) {
-        if (EPI == EPI_SWIGLU) {
+        if (is_up(EPI)) {
             constexpr int HW = BN / 2 / WN;  // h columns per wave
             const int half = nt / (NTW / 2), i = nt % (NTW / 2);
             return half * (BN / 2) + wn * HW + 32 * i;
@@ -589,7 +603,7 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
             if (LB == LAY_MN) {
                 const uint32_t range = (uint32_t)((p.Kd - kofs) * p.ldw * 2);
                 c_srdB0 = make_srd(p.w0 + (int64_t)ic.j * p.w_stride + kofs * p.ldw, range);
-                if (EPI == EPI_SWIGLU) c_srdB1 = make_srd(p.w1 + (int64_t)ic.j * p.w_stride + kofs * p.ldw, range);
+                if (is_up(EPI)) c_srdB1 = make_srd(p.w1 + (int64_t)ic.j * p.w_stride + kofs * p.ldw, range);
             } else {
                 const int n0 = ic.ni * BN;
                 const uint32_t range = (uint32_t)((min(BN, p.N - n0) * p.ldw - kofs) * 2);
@@ -764,7 +778,7 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
                     const int sub = mn_sub(u - LA);
                     i32x4 r;
                     int col;
-                    if (EPI == EPI_SWIGLU) {
+                    if (is_up(EPI)) {
                         constexpr int HS = BN / 128;  // sub-tiles per half
                         r = sub < HS ? c_srdB0 : c_srdB1;
                         col = ic.ni * (BN / 2) + (sub % HS) * 64;
@@ -1008,8 +1022,10 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
                 }
                 continue;
             }
-            static_assert(EPI == EPI_SWIGLU_BWD || SCHED == SCHED_WGRAD, "16x16x32 body: the down dgrad or dW");
-            if constexpr (EPI == EPI_SWIGLU_BWD && MOE_GEMM_DGRAD_STAGED) {  // the accumulators are dh
+            constexpr bool kBwd8 = EPI == EPI_SWIGLU_BWD8;
+            static_assert(EPI == EPI_SWIGLU_BWD || kBwd8 || SCHED == SCHED_WGRAD,
+                          "16x16x32 body: the down dgrad or dW");
+            if constexpr (kBwd8 || (EPI == EPI_SWIGLU_BWD && MOE_GEMM_DGRAD_STAGED)) {  // the accumulators are dh
                 // The saved (a, b) pairs come in, and (da, db) go out, as whole
                 // 256-byte row pieces through the wave's 8 KiB of the free slot:
                 // one 16-row block at a time, a in its first 4 KiB and b in the
@@ -1028,18 +1044,40 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
                 const int ncol = ni * BN + wn * (BN / WN) + 8 * cc;  // the chunk's first column
                 const bool col_ok = ncol < p.N;
                 constexpr int kPre = MOE_GEMM_DGRAD_PREFETCH;
-                u32x4 ld[kPre][2][4];
+                // SWIGLU_BWD8: 8 bytes and the block's scale byte per chunk of 8
+                // columns, widened to bf16 (exactly) on the way into LDS
+                typedef std::conditional_t<kBwd8, u32x2, u32x4> Saved;
+                Saved ld[kPre][2][4];
+                uint32_t ls[kBwd8 ? kPre : 1][2][4];
                 auto issue_loads = [&](int m) {
-                    u32x4(&l)[2][4] = ld[m % kPre];
+                    Saved(&l)[2][4] = ld[m % kPre];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int mloc = row16(m) + 4 * i + rw;
-                        l[0][i] = l[1][i] = u32x4{0u, 0u, 0u, 0u};
+                        l[0][i] = l[1][i] = Saved{};
+                        if constexpr (kBwd8) ls[m % kPre][0][i] = ls[m % kPre][1][i] = 127u;
                         if (mloc < valid && col_ok) {
-                            const uint16_t* src = p.ab + (int64_t)(row0 + mloc) * 2 * p.N + ncol;
-                            l[0][i] = *(const u32x4*)src;
-                            l[1][i] = *(const u32x4*)(src + p.N);
+                            const int64_t at = (int64_t)(row0 + mloc) * 2 * p.N + ncol;
+                            if constexpr (kBwd8) {
+                                l[0][i] = *(const u32x2*)(p.q8 + at);
+                                l[1][i] = *(const u32x2*)(p.q8 + at + p.N);
+                                ls[m % kPre][0][i] = p.s8[at >> 5];
+                                ls[m % kPre][1][i] = p.s8[(at + p.N) >> 5];
+                            } else {
+                                l[0][i] = *(const u32x4*)(p.ab + at);
+                                l[1][i] = *(const u32x4*)(p.ab + at + p.N);
+                            }
                         }
+                    }
+                };
+                auto saved_bf16 = [&](int m, int hb, int i) {
+                    if constexpr (kBwd8) {
+                        const float step = step8(ls[m % kPre][hb][i]);
+                        const u32x2 lo = dequant8x4(ld[m % kPre][hb][i][0], step);
+                        const u32x2 hi = dequant8x4(ld[m % kPre][hb][i][1], step);
+                        return u32x4{lo[0], lo[1], hi[0], hi[1]};
+                    } else {
+                        return ld[m % kPre][hb][i];
                     }
                 };
                 // MFMA layout: row ln%16, columns 4q..4q+3 of each 16-column block
@@ -1058,15 +1096,16 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
 #pragma unroll
                     for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) *(MOE_LDS u32x4*)sa(hb, 4 * i + rw, cc) = ld[m % kPre][hb][i];
+                        for (int i = 0; i < 4; ++i) *(MOE_LDS u32x4*)sa(hb, 4 * i + rw, cc) = saved_bf16(m, hb, i);
                     asm volatile("" ::: "memory");  // a wave's LDS accesses execute in order
                     if (m + kPre < MB16) issue_loads(m + kPre);
+                    u32x2 hw[kBwd8 ? NB16 : 1];  // the block's h values, for dW_down
 #pragma unroll
                     for (int nb = 0; nb < NB16; ++nb) {
                         MOE_LDS uint8_t* pa = sa(0, r, 2 * nb + (q >> 1)) + 8 * (q & 1);
                         MOE_LDS uint8_t* pb = sa(1, r, 2 * nb + (q >> 1)) + 8 * (q & 1);
                         const u32x2 aw = *(const MOE_LDS u32x2*)pa, bw = *(const MOE_LDS u32x2*)pb;
-                        float da[4], db[4];
+                        float da[4], db[4], hv[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const float v = acc16[m][nb][i];
@@ -1077,7 +1116,9 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
                             const float u = v * sg, w = u * b;
                             db[i] = u * a;
                             da[i] = __builtin_fmaf(w, __builtin_fmaf(-a, sg, a), w);
+                            if constexpr (kBwd8) hv[i] = a * sg * b;
                         }
+                        if constexpr (kBwd8) hw[nb] = u32x2{pack_bf2x(hv[0], hv[1]), pack_bf2x(hv[2], hv[3])};
                         *(MOE_LDS u32x2*)pa = u32x2{pack_bf2x(da[0], da[1]), pack_bf2x(da[2], da[3])};
                         *(MOE_LDS u32x2*)pb = u32x2{pack_bf2x(db[0], db[1]), pack_bf2x(db[2], db[3])};
                     }
@@ -1092,6 +1133,23 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
                                 *(u32x4*)(p.c + (int64_t)(row0 + mloc) * p.ldc + hb * p.N + ncol) = v;
                         }
                     asm volatile("" ::: "memory");  // this block's rows are read before the next is written
+                    if constexpr (kBwd8) {
+                        if (p.c2) {
+                            // h takes the same way out
+#pragma unroll
+                            for (int nb = 0; nb < NB16; ++nb)
+                                *(MOE_LDS u32x2*)(sa(0, r, 2 * nb + (q >> 1)) + 8 * (q & 1)) = hw[nb];
+                            asm volatile("" ::: "memory");
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const u32x4 v = *(const MOE_LDS u32x4*)sa(0, 4 * i + rw, cc);
+                                const int mloc = row16(m) + 4 * i + rw;
+                                if (mloc < valid && col_ok)
+                                    *(u32x4*)(p.c2 + (int64_t)(row0 + mloc) * p.N + ncol) = v;
+                            }
+                            asm volatile("" ::: "memory");
+                        }
+                    }
                 }
                 __syncthreads();  // every wave is done with the slot before the next stage refills it
             } else if constexpr (EPI == EPI_SWIGLU_BWD) {  // the accumulators are dh
@@ -1438,6 +1496,104 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
                         }
                     }
                 }
+            } else if constexpr (EPI == EPI_SWIGLU8) {
+                // a 32-column block of a row is in lanes l and l ^ 32
+#pragma unroll
+                for (int i2 = 0; i2 < NTW / 2; ++i2) {
+                    const f32x16& ga = acc[mt][i2];
+                    const f32x16& ub = acc[mt][NTW / 2 + i2];
+                    const int hc0 = ni * (BN / 2) + col_of(i2);
+                    if (hc0 >= p.N) continue;
+#pragma unroll
+                    for (int j4 = 0; j4 < 4; ++j4) {
+                        float hv[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) hv[i] = silu_f(ga[4 * j4 + i]) * ub[4 * j4 + i];
+                        u32x2 hw = {pack_bf2x(hv[0], hv[1]), pack_bf2x(hv[2], hv[3])};
+                        *(u32x2*)(p.c + row * p.ldc + hc0 + 8 * j4 + cq) = hw;
+                    }
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const f32x16& v = half ? ub : ga;
+                        uint32_t w[8], m = 0;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            w[i] = pack_bf2x(v[2 * i], v[2 * i + 1]);
+                            m = max_mag2(m, w[i] & 0x7fff7fffu);
+                        }
+                        m = max(m & 0xffffu, m >> 16);
+                        m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+                        const uint32_t sc = scale8_of(m);
+                        const float inv = inv_step8(sc);
+                        uint32_t d[4];
+#pragma unroll
+                        for (int j4 = 0; j4 < 4; ++j4) {
+                            d[j4] = quant8x4(bf_lo(w[2 * j4]), bf_hi(w[2 * j4]), bf_lo(w[2 * j4 + 1]),
+                                             bf_hi(w[2 * j4 + 1]), inv);
+                            if (sc == 255u) d[j4] = 0u;
+                        }
+                        // the lower half-wave takes columns 0..15, the upper 16..31
+                        const auto e0 = __builtin_amdgcn_permlane32_swap(d[0], d[2], false, false);
+                        const auto e1 = __builtin_amdgcn_permlane32_swap(d[1], d[3], false, false);
+                        const int64_t at = row * 2 * p.N + half * p.N + hc0;
+                        *(u32x4*)(p.q8 + at + 4 * cq) = u32x4{e0[0], e0[1], e1[0], e1[1]};
+                        if (cq == 0) p.s8[at >> 5] = (uint8_t)sc;
+                    }
+                }
+            } else if constexpr (EPI == EPI_SWIGLU_BWD8) {  // the accumulators are dh
+                uint32_t aw[NTW][4], bw[NTW][4], as[NTW], bs[NTW];
+#pragma unroll
+                for (int nt = 0; nt < NTW; ++nt) {
+                    const int n0 = ni * BN + col_of(nt);
+                    const int64_t at = row * 2 * p.N + n0;
+                    as[nt] = bs[nt] = 127u;
+                    if (n0 < p.N) {
+                        as[nt] = p.s8[at >> 5];
+                        bs[nt] = p.s8[(at + p.N) >> 5];
+                    }
+#pragma unroll
+                    for (int j4 = 0; j4 < 4; ++j4) {
+                        aw[nt][j4] = bw[nt][j4] = 0u;
+                        if (n0 < p.N) {
+                            aw[nt][j4] = *(const uint32_t*)(p.q8 + at + 8 * j4 + cq);
+                            bw[nt][j4] = *(const uint32_t*)(p.q8 + at + p.N + 8 * j4 + cq);
+                        }
+                    }
+                }
+                // all loaded before the first store, as below
+#pragma unroll
+                for (int nt = 0; nt < NTW; ++nt) {
+                    asm volatile("" ::"v"(as[nt]), "v"(bs[nt]));
+#pragma unroll
+                    for (int j4 = 0; j4 < 4; ++j4) asm volatile("" ::"v"(aw[nt][j4]), "v"(bw[nt][j4]));
+                }
+#pragma unroll
+                for (int nt = 0; nt < NTW; ++nt) {
+                    const float sta = step8(as[nt]), stb = step8(bs[nt]);
+#pragma unroll
+                    for (int j4 = 0; j4 < 4; ++j4) {
+                        const int n = ni * BN + col_of(nt) + 8 * j4 + cq;
+                        if (n >= p.N) continue;
+                        const u32x2 a2 = dequant8x4(aw[nt][j4], sta), b2 = dequant8x4(bw[nt][j4], stb);
+                        float da[4], db[4], hv[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float v = acc[mt][nt][4 * j4 + i];
+                            const float a = (i & 1) ? bf_hi(a2[i >> 1]) : bf_lo(a2[i >> 1]);
+                            const float b = (i & 1) ? bf_hi(b2[i >> 1]) : bf_lo(b2[i >> 1]);
+                            const float sg = sigmoid_f(a);
+                            const float u = v * sg, w = u * b;
+                            db[i] = u * a;
+                            da[i] = __builtin_fmaf(w, __builtin_fmaf(-a, sg, a), w);
+                            hv[i] = a * sg * b;
+                        }
+                        *(u32x2*)(p.c + row * p.ldc + n) = u32x2{pack_bf2x(da[0], da[1]), pack_bf2x(da[2], da[3])};
+                        *(u32x2*)(p.c + row * p.ldc + p.N + n) =
+                            u32x2{pack_bf2x(db[0], db[1]), pack_bf2x(db[2], db[3])};
+                        if (p.c2)
+                            *(u32x2*)(p.c2 + row * p.N + n) = u32x2{pack_bf2x(hv[0], hv[1]), pack_bf2x(hv[2], hv[3])};
+                    }
+                }
             } else if (EPI == EPI_BF16) {
 #pragma unroll
                 for (int nt = 0; nt < NTW; ++nt)
@@ -1525,7 +1681,7 @@ __device__ __forceinline__ bool prefer_alt(const GemmParams& p, const int* s_off
         ma += s_wave[2 * w + 1];
     }
     __syncthreads();  // s_wave is reused by the schedule
-    const int64_t tn = EPI == EPI_SWIGLU ? (p.N + BN / 2 - 1) / (BN / 2) : (p.N + BN - 1) / BN;
+    const int64_t tn = is_up(EPI) ? (p.N + BN / 2 - 1) / (BN / 2) : (p.N + BN - 1) / BN;
     const int64_t G = gridDim.x;
     const int64_t rb = (mb * tn + G - 1) / G, ra = (ma * tn + G - 1) / G;
     return ra * ALT * 11 < rb * BM * 10;
@@ -1594,7 +1750,7 @@ void gg_kernel(GemmParams p) {
     // for outputs whose every tile is whole (all the layer's workloads)
     constexpr bool kFullBody = BM == 256 && BN == 256;
     const bool fullc = kFullBody && (SCHED == SCHED_WGRAD ? p.M % BM == 0 && p.N % BN == 0
-                                                          : p.N % (EPI == EPI_SWIGLU ? BN / 2 : BN) == 0);
+                                                          : p.N % (is_up(EPI) ? BN / 2 : BN) == 0);
     if constexpr (kNtPath) {
         if (max_rows <= BM) {
             if constexpr (kFullBody) {
@@ -1649,7 +1805,7 @@ static int launch_cfg(const GemmParams& p, hipStream_t s) {
     using TL = Tile<BM, BN, BK, WM, WN, LDSB>;
     int64_t total_upper;
     if (SCHED == SCHED_ROWS) {
-        const int tn = EPI == EPI_SWIGLU ? (p.N + BN / 2 - 1) / (BN / 2) : (p.N + BN - 1) / BN;
+        const int tn = is_up(EPI) ? (p.N + BN / 2 - 1) / (BN / 2) : (p.N + BN - 1) / BN;
         constexpr int bm = ALT && ALT < BM ? ALT : BM;
         total_upper = ((p.cap + bm - 1) / bm + p.e_local) * (int64_t)tn * std::max(p.ksplit, 1);
     } else {

@@ -43,9 +43,15 @@ class MoeBuffers:
     # zero-copy dispatch: the permutation is index-only, and the gate/up
     # GroupGEMM and the gate/up weight gradient read x[src[r] // K]
     zero_copy: bool = False
+    # 8-bit checkpoint: the forward saves (a, b) in 8-bit blocks instead of ab, and the backward recomputes
+    # h from them, so h is scratch that layers may share
+    checkpoint8: bool = False
+    ab8: torch.Tensor | None = None
+    ab8_scale: torch.Tensor | None = None
 
     @classmethod
-    def allocate(cls, shape: MoeShape, cap: int | None = None, device="cuda", backward=None, zero_copy=False):
+    def allocate(cls, shape: MoeShape, cap: int | None = None, device="cuda", backward=None, zero_copy=False,
+                 checkpoint8=False):
         backward = shape.backward if backward is None else backward
         T, H, F, K, EL = shape.T, shape.H, shape.F, shape.K, shape.EL
         cap = shape.cap if cap is None else cap
@@ -58,7 +64,11 @@ class MoeBuffers:
                 pos=e((T, K), dt=torch.int32), src=e(capn, dt=torch.int32),
                 x_perm=None if zero_copy else e((capn, H)),
                 status=e(4, dt=torch.int32), ws=e(ws_bytes, dt=torch.uint8), h=e((capn, F)),
-                ab=e((capn, 2 * F)) if backward else None, y=e((capn, H)), out=e((T, H)), zero_copy=zero_copy)
+                ab=e((capn, 2 * F)) if backward and not checkpoint8 else None, y=e((capn, H)), out=e((T, H)),
+                zero_copy=zero_copy, checkpoint8=checkpoint8 and backward)
+        if b.checkpoint8:
+            b.ab8 = e((capn, 2 * F), dt=torch.int8)
+            b.ab8_scale = e((capn, 2 * F // 32), dt=torch.uint8)
         if backward:
             b.dy_perm = e((capn, H))
             b.dab = e((capn, 2 * F))
@@ -85,7 +95,14 @@ def permute(buf: MoeBuffers, x):
 
 def expert_up(buf: MoeBuffers, w_gate, w_up, x=None):
     """x (the token rows) is needed with zero_copy only."""
-    if buf.zero_copy:
+    if buf.checkpoint8:
+        if buf.zero_copy:
+            _lib.moe_grouped_gemm_swiglu_gather_save8(x, buf.src, buf.shape.K, w_gate, w_up, buf.offsets, buf.cap,
+                                                      h=buf.h, ab8=buf.ab8, ab8_scale=buf.ab8_scale)
+        else:
+            _lib.moe_grouped_gemm_swiglu_save8(buf.x_perm, w_gate, w_up, buf.offsets, buf.cap, h=buf.h,
+                                               ab8=buf.ab8, ab8_scale=buf.ab8_scale)
+    elif buf.zero_copy:
         _lib.moe_grouped_gemm_swiglu_gather(x, buf.src, buf.shape.K, w_gate, w_up, buf.offsets, buf.cap,
                                             h=buf.h, ab_save=buf.ab)
     else:
@@ -111,15 +128,38 @@ def forward(buf: MoeBuffers, inp: dict):
     return buf.out
 
 
+def pack_weights4(inp: dict) -> dict:
+    """The experts' weights in 4-bit blocks, once per model: (q4, s4) pairs for forward4."""
+    return {k + "4": _lib.moe_pack4(inp[k]) for k in ("w_gate", "w_up", "w_down")}
+
+
+def forward4(buf: MoeBuffers, inp: dict):
+    """The forward of a decode step on 4-bit weights. inp: device tensors logits and x, and pack_weights4's
+    pairs. The products read the tokens through src, so the buffers are zero-copy ones."""
+    s = buf.shape
+    if not buf.zero_copy:
+        raise _lib.MoeError("forward4: the buffers need zero_copy=True")
+    route(buf, inp["logits"])
+    permute(buf, inp["x"])
+    _lib.moe_grouped_gemm4_swiglu(inp["x"], buf.src, s.K, inp["w_gate4"], inp["w_up4"], buf.offsets, buf.cap, h=buf.h)
+    _lib.moe_grouped_gemm4(buf.h, inp["w_down4"], buf.offsets, buf.cap, c=buf.y)
+    combine(buf)
+    return buf.out
+
+
 def backward(buf: MoeBuffers, inp: dict):
     """inp additionally holds d_out (and x, read by the zero-copy weight gradient). Needs the forward's
-    ab_save."""
+    ab_save, or its 8-bit (a, b), from which h is recomputed into buf.h."""
     s = buf.shape
     H, F, EL, cap = s.H, s.F, s.EL, buf.cap
     _lib.moe_gather_gate_grad(inp["d_out"], buf.pos, buf.gates, buf.y, buf.dy_perm, buf.dgates)
     _lib.moe_route_backward(buf.topk_idx, buf.gates, buf.dgates, s.E, buf.dlogits)
-    _lib.moe_grouped_gemm(buf.dy_perm, inp["w_down"], None, 1, buf.offsets, H, F, cap, buf.dab,
-                          epilogue=_lib.MOE_EPI_SWIGLU_BWD, ab=buf.ab)
+    if buf.checkpoint8:
+        _lib.moe_grouped_gemm_swiglu_bwd8(buf.dy_perm, inp["w_down"], buf.offsets, cap, buf.ab8, buf.ab8_scale,
+                                          dab=buf.dab, h=buf.h)
+    else:
+        _lib.moe_grouped_gemm(buf.dy_perm, inp["w_down"], None, 1, buf.offsets, H, F, cap, buf.dab,
+                              epilogue=_lib.MOE_EPI_SWIGLU_BWD, ab=buf.ab)
     _lib.moe_grouped_gemm(buf.dab, inp["w_gate"], inp["w_up"], 1, buf.offsets, F, H, cap, buf.dx_perm)
     _lib.moe_combine(buf.dx_perm, buf.pos, None, out=buf.dx)
     if buf.zero_copy:
