@@ -457,7 +457,7 @@ int moe_unpack4(const uint8_t* q4, const uint8_t* s4, int E, int Kd, int N, moe_
 /*
  * Gate/up and down products on 4-bit weights, for the few rows per expert of
  * a decode step (one token to some hundreds): every weight byte of an expert
- * with rows is read once per 16 to 64 of them.  Rows, offsets and results as
+ * with rows is read once per 16 or 32 of them.  Rows, offsets and results as
  * in the bf16 products, with the packed weights' values for w:
  *   h[r] = bf16(silu(x_r . w_gate[j]) * (x_r . w_up[j])),   c[r] = bf16(a[r] . w[j])
  * with x_r = x[src[r] / K], or x[r] if src is NULL (x then has cap_rows rows in
@@ -474,6 +474,21 @@ int moe_grouped_gemm4_swiglu(const moe_bf16* x, int T, const int32_t* src, int K
                              moe_stream stream);
 int moe_grouped_gemm4(const moe_bf16* a, const uint8_t* q4, const uint8_t* s4, const int32_t* offsets, int e_local,
                       int Kd, int N, int cap_rows, moe_bf16* c, moe_stream stream);
+
+/*
+ * moe_grouped_gemm4 and moe_combine in one, without rounding the experts' rows
+ * to bf16 in between:
+ *   out[t] = bf16(sum over k ascending with 0 <= pos[t,k] < cap_rows of gates[t,k] * (a[pos[t,k]] . w))
+ * A token without such a pair gets +0.  y, if not NULL, is moe_grouped_gemm4's c.
+ *   pos int32 [T,K], gates fp32 [T,K];  y bf16 [cap_rows,N] or NULL;  out bf16 [T,N];
+ *   ws: device workspace of at least moe_gemm4_combine_workspace_size(cap_rows, N)
+ *   bytes (the fp32 rows).  T <= 262140; MOE_EWORKSPACE if ws is NULL or too small.
+ */
+size_t moe_gemm4_combine_workspace_size(int cap_rows, int N);
+int moe_grouped_gemm4_combine(const moe_bf16* a, const uint8_t* q4, const uint8_t* s4, const int32_t* offsets,
+                              int e_local, int Kd, int N, int cap_rows, const int32_t* pos, const float* gates,
+                              int T, int K, moe_bf16* y, moe_bf16* out, void* ws, size_t ws_bytes,
+                              moe_stream stream);
 
 /*
  * Measurement aid, not a step of the layer: the bf16 MFMA rate this GPU

@@ -51,6 +51,8 @@ SIGNATURES = {
     "moe_unpack4": ([_p, _p, _i, _i, _i, _p, _p], _i),
     "moe_grouped_gemm4_swiglu": ([_p, _i, _p, _i, _p, _p, _p, _p, _p, _i, _i, _i, _i, _p, _p], _i),
     "moe_grouped_gemm4": ([_p, _p, _p, _p, _i, _i, _i, _i, _p, _p], _i),
+    "moe_gemm4_combine_workspace_size": ([_i, _i], _z),
+    "moe_grouped_gemm4_combine": ([_p, _p, _p, _p, _i, _i, _i, _i, _p, _p, _i, _i, _p, _p, _p, _z, _p], _i),
     "moe_probe_mfma": ([_p, _i, _i, _p, _p], _i),
     "moe_probe_mfma16": ([_p, _i, _i, _p, _p], _i),
     "moe_probe_copy": ([_p, _p, _i64, _i, _i, _p], _i),
@@ -740,6 +742,44 @@ def moe_grouped_gemm4(a, w, offsets, cap_rows, c=None, stream=None):
     _check(load().moe_grouped_gemm4(_ptr(a), _ptr(q4), _ptr(s4), _ptr(offsets), EL, Kd, N, cap_rows, _ptr(c),
                                     _stream(stream)))
     return c
+
+
+def moe_gemm4_combine_workspace_size(cap_rows, N) -> int:
+    return int(load().moe_gemm4_combine_workspace_size(cap_rows, N))
+
+
+def moe_grouped_gemm4_combine(a, w, offsets, cap_rows, pos, gates, y=None, out=None, ws=None, stream=None):
+    """out[t] = sum_k gates[t,k] * (a[pos[t,k]] . w) on 4-bit weights, the experts' rows kept in fp32 (ws) until
+    the one rounding of out; y (optional): those rows in bf16, as moe_grouped_gemm4 gives them."""
+    _need(a, torch.bfloat16, "a")
+    _need(offsets, torch.int32, "offsets")
+    _need(pos, torch.int32, "pos")
+    _need(gates, torch.float32, "gates")
+    if a.dim() != 2 or a.shape[0] < cap_rows:
+        raise MoeError(f"a: expected at least {cap_rows} rows, got {tuple(a.shape)}")
+    Kd = a.shape[1]
+    q4, s4, EL, N = _weights4(w, Kd, "w")
+    if offsets.numel() < EL + 1:
+        raise MoeError(f"offsets: expected {EL + 1} entries, got {offsets.numel()}")
+    if pos.dim() != 2:
+        raise MoeError(f"pos: expected [T, K], got {tuple(pos.shape)}")
+    T, K = pos.shape
+    _shape(gates, (T, K), "gates")
+    if y is not None:
+        _need(y, torch.bfloat16, "y")
+        _rows(y, cap_rows, N, "y")
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=a.device)
+    _need(out, torch.bfloat16, "out")
+    _shape(out, (T, N), "out")
+    need = moe_gemm4_combine_workspace_size(cap_rows, N)
+    if ws is None or ws.numel() < need:
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=a.device)
+    _need(ws, torch.uint8, "ws")
+    _check(load().moe_grouped_gemm4_combine(_ptr(a), _ptr(q4), _ptr(s4), _ptr(offsets), EL, Kd, N, cap_rows,
+                                            _ptr(pos), _ptr(gates), T, K, _ptr(y), _ptr(out), _ptr(ws), ws.numel(),
+                                            _stream(stream)))
+    return out
 
 
 def moe_probe_mfma(operands, iters, out=None, stream=None):

@@ -5,22 +5,27 @@
 // for the rows r of expert j, W the bf16 values of the packed weights (mx.hpp)
 // and fp32 sums.  A token meets a handful of experts, so almost every byte
 // moved is a weight, read once: the time is that of streaming 17/32 byte a
-// weight, and the kernel's work is to keep enough of those bytes in flight.
+// weight, and the kernels' work is to keep enough of those bytes in flight.
 //
 // Packed tiles hold 16 output columns x 128 contraction values in 1 KiB, in
 // the order of the matrix instruction's first operand: lane l of a wave owns
 // the block of 32 contraction values 32*(l/16) .. +31 of column l%16, one
 // 16-byte load, one scale byte and 16 conversions (each exact: a 4-bit value
 // times a power of two is a bf16) for four v_mfma_f32_16x16x32_bf16.  The
-// rows are the second operand: lane l holds the same 32 contraction values of
-// row l%16, 64 contiguous bytes.  The four steps of a tile take 8 values from
-// every lane group, so the contraction order inside a tile is a fixed
-// permutation of the natural one.
+// rows are the second operand: lane l needs the same 32 contraction values of
+// row l%16.  The four steps of a tile take 8 values from every lane group, so
+// the contraction order inside a tile is a fixed permutation of the natural
+// one.
 //
-// A workgroup computes 16*MT rows x 16*NT columns (of both matrices for
-// gate/up); its W waves take the contraction tiles in turn and their fp32
-// sums meet in LDS, added in wave order.  No LDS is used on the way in: a
-// weight byte has one reader, and the rows are read once per workgroup.
+// Two kernels share this:
+//   gemm4_split: the waves of a workgroup take the contraction tiles of the
+//     same 16 rows x 16*NT columns in turn; their fp32 sums meet in LDS, added
+//     in wave order.  For one token or two, whose tiles are too few to give
+//     every SIMD a wave of its own columns.
+//   gemm4_wide: every wave has its own 16*NT columns and runs the whole
+//     contraction; the rows, which the waves share, go through LDS.  Nothing is
+//     reduced across waves, and a row byte is read once per 64*NT columns.
+// The rule between them is in launch4_rows.
 #include "mx.hpp"
 
 namespace moe {
@@ -37,31 +42,29 @@ struct Gemm4Params {
     int e_local;
     int64_t cap;
     int Kd, N, KT;
-    uint16_t* c;         // [cap, N]
+    uint16_t* c;         // bf16 [cap, N], or NULL
+    float* c32;          // fp32 [cap, N], or NULL
 };
 
 // Per-lane byte offset that is outside every resource (those of tokens may
 // reach 3.75 GiB), also with any column offset of a row added.
 constexpr uint32_t kNoRow = kOOB_GATHER;
 
-template <int MATS, int MT, int NT, int W>
-__global__ __launch_bounds__(64 * W) void gemm4_kernel(Gemm4Params p) {
-    constexpr int ACC = MATS * NT * MT;
-    __shared__ f32x4 part[W][ACC][64];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-
-    // ---- this workgroup's tile, from the device-resident row counts ----
-    // Lane l counts the row tiles of experts l*per .. l*per+per-1.
-    constexpr int BM = 16 * MT;
-    const int per = (p.e_local + 63) >> 6;
-    int mine = 0;
-    for (int i = 0; i < per; ++i) {
-        const int j = lane * per + i;
-        if (j < p.e_local) {
-            const int64_t lo = min((int64_t)p.offsets[j], p.cap), hi = min((int64_t)p.offsets[j + 1], p.cap);
-            mine += (int)((hi - lo + BM - 1) / BM);
-        }
+// The tile of this workgroup, the same in every lane (j = -1: none).  Lane l
+// holds the row tiles of experts l*PER .. l*PER+PER-1.
+template <int PER, int BM>
+__device__ __forceinline__ void find_tile(const Gemm4Params& p, int lane, int slabs, int& j, int& row0, int& rows,
+                                          int& slab) {
+    int at[PER + 1];
+#pragma unroll
+    for (int i = 0; i <= PER; ++i) at[i] = p.offsets[min(lane * PER + i, p.e_local)];
+    int n[PER], mine = 0;
+#pragma unroll
+    for (int i = 0; i <= PER; ++i) at[i] = (int)min((int64_t)at[i], p.cap);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        n[i] = (at[i + 1] - at[i] + BM - 1) / BM;
+        mine += n[i];
     }
     int incl = mine;
 #pragma unroll
@@ -70,117 +73,180 @@ __global__ __launch_bounds__(64 * W) void gemm4_kernel(Gemm4Params p) {
         if (lane >= o) incl += t;
     }
     const int tiles = __builtin_amdgcn_readlane(incl, 63);
-    const int slabs = (p.N / 16 + NT - 1) / NT;
     // workgroup b runs on XCD b % 8: each XCD takes a contiguous run, in which
     // an expert's row tiles of one slab (the same weights) are neighbours
     const int run = (tiles * slabs + 7) >> 3;
-    const int at = (int)(blockIdx.x >> 3);
-    const int id = (int)(blockIdx.x & 7) * run + at;
-    if (at >= run || id >= tiles * slabs) return;
-    const int slab = id / tiles;
-    int rest = id - slab * tiles;
-    const uint64_t has = __ballot(incl > rest);  // the first lane with more tiles up to it
-    const int owner = __builtin_ctzll(has);
-    rest -= __builtin_amdgcn_readlane(incl - mine, owner);
-    int j = owner * per, row0 = 0, rows = 0;
-    for (int i = 0; i < per; ++i) {
-        const int jj = owner * per + i;
-        const int64_t lo = min((int64_t)p.offsets[jj], p.cap), hi = min((int64_t)p.offsets[jj + 1], p.cap);
-        const int n = (int)((hi - lo + BM - 1) / BM);
-        if (rest < n) {
-            j = jj;
-            row0 = (int)lo + rest * BM;
-            rows = min(BM, (int)(hi - row0));
-            break;
-        }
-        rest -= n;
-    }
-    j = __builtin_amdgcn_readfirstlane(j);
-    row0 = __builtin_amdgcn_readfirstlane(row0);
-    rows = __builtin_amdgcn_readfirstlane(rows);
-
-    // ---- the rows: a byte offset per lane and 16-row block ----
-    const int r16 = lane & 15, g = lane >> 4;
-    const uint32_t ld = (uint32_t)p.Kd * 2u;
-    const bool gather = p.src != nullptr;
-    const uint16_t* base = gather ? p.a : p.a + (int64_t)row0 * p.Kd;
-    const auto rs = make_rsrc(base, gather ? (uint32_t)(p.a_rows * p.Kd * 2) : (uint32_t)rows * ld);
-    uint32_t off[MT];
+    const int b = (int)(blockIdx.x >> 3);
+    const int id = (int)(blockIdx.x & 7) * run + b;
+    if (b >= run || id >= tiles * slabs) return;
+    slab = id / tiles;
+    const int tile = id - slab * tiles;
+    const int owner = __builtin_ctzll(__ballot(incl > tile));  // the first lane with more tiles up to it
+    int rest = tile - (incl - mine), jj = 0, r0 = 0, end = 0;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int r = 16 * m + r16;
-        off[m] = kNoRow;
-        if (r < rows) {
-            uint32_t tok = (uint32_t)r;
-            if (gather) {
-                const uint32_t v = (uint32_t)p.src[row0 + r];
-                tok = __umulhi(v, p.topk_rcp);  // the quotient, or one less
-                if (v - tok * (uint32_t)p.topk >= (uint32_t)p.topk) ++tok;
-            }
-            if (!gather || tok < (uint64_t)p.a_rows) off[m] = tok * ld + 64u * g;
+    for (int i = 0; i < PER; ++i) {
+        if (rest >= 0 && rest < n[i]) {
+            jj = lane * PER + i;
+            r0 = at[i] + rest * BM;
+            end = at[i + 1];
         }
+        rest -= n[i];
     }
+    j = __builtin_amdgcn_readlane(jj, owner);
+    row0 = __builtin_amdgcn_readlane(r0, owner);
+    rows = min(BM, __builtin_amdgcn_readlane(end, owner) - row0);
+}
 
-    // ---- contraction ----
-    const int nt0 = slab * NT;
-    const int64_t tile0 = ((int64_t)j * (p.N >> 4) + nt0) * p.KT;
-    struct Stage {
-        u32x4 w[MATS][NT];
-        uint32_t s[MATS][NT];
-        u32x4 x[MT][4];
-    };
-    auto load = [&](Stage& t, int kt) {
+// 4 x 4 transpose between register index and lane group of 16 (16 bytes each):
+// v[t] of group g becomes what v[g] of group t was.
+__device__ __forceinline__ void transpose4(u32x4 (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const auto a = __builtin_amdgcn_permlane32_swap(v[0][i], v[2][i], false, false);
+        const auto b = __builtin_amdgcn_permlane32_swap(v[1][i], v[3][i], false, false);
+        const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+        const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+        v[0][i] = c[0];
+        v[1][i] = c[1];
+        v[2][i] = d[0];
+        v[3][i] = d[1];
+    }
+}
+
+template <int BM>
+__device__ __forceinline__ void find_tile_of(const Gemm4Params& p, int lane, int slabs, int& j, int& row0, int& rows,
+                                             int& slab) {
+    j = -1;
+    if (p.e_local <= 64) find_tile<1, BM>(p, lane, slabs, j, row0, rows, slab);
+    else if (p.e_local <= 128) find_tile<2, BM>(p, lane, slabs, j, row0, rows, slab);
+    else if (p.e_local <= 256) find_tile<4, BM>(p, lane, slabs, j, row0, rows, slab);
+    else find_tile<8, BM>(p, lane, slabs, j, row0, rows, slab);
+}
+
+// The resource that a tile's rows are read through (rows past it read 0), and
+// the byte offset in it of the tile's row r.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const Gemm4Params& p, int row0, int rows) {
+    if (p.src) return make_rsrc(p.a, (uint32_t)(p.a_rows * p.Kd * 2));
+    return make_rsrc(p.a + (int64_t)row0 * p.Kd, (uint32_t)rows * ((uint32_t)p.Kd * 2u));
+}
+__device__ __forceinline__ uint32_t row_offset(const Gemm4Params& p, int row0, int rows, int r) {
+    if (r >= rows) return kNoRow;
+    uint32_t tok = (uint32_t)r;
+    if (p.src) {
+        const uint32_t v = (uint32_t)p.src[row0 + r];
+        tok = __umulhi(v, p.topk_rcp);  // the quotient, or one less
+        if (v - tok * (uint32_t)p.topk >= (uint32_t)p.topk) ++tok;
+        if (tok >= (uint64_t)p.a_rows) return kNoRow;
+    }
+    return tok * ((uint32_t)p.Kd * 2u);
+}
+
+// First packed tile of each of the NT column tiles from nt0 of expert j (column
+// tiles past the last are taken as the last; their results are not stored).
+template <int NT>
+__device__ __forceinline__ void column_tiles(const Gemm4Params& p, int j, int nt0, int64_t (&at)[NT]) {
+    const int n = p.N >> 4;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) at[i] = ((int64_t)j * n + min(nt0 + i, n - 1)) * p.KT;
+}
+
+// One contraction tile of a wave's weights: NT column tiles of each matrix.
+template <int MATS, int NT>
+struct Weights4 {
+    u32x4 w[MATS][NT];
+    uint32_t s[MATS][NT];
+    template <bool NTL>
+    __device__ __forceinline__ void load(const Gemm4Params& p, const int64_t (&at)[NT], int kt, int lane) {
 #pragma unroll
         for (int q = 0; q < MATS; ++q)
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                const bool in = NT == 1 || nt0 + i < (p.N >> 4);
-                const int64_t tile = tile0 + (in ? (int64_t)i * p.KT : 0) + kt;
-                t.w[q][i] = *(const u32x4*)(p.q[q] + tile * 1024 + lane * 16);
-                t.s[q][i] = p.s[q][tile * 64 + lane];
+                const int64_t tile = at[i] + kt;
+                const u32x4* src = (const u32x4*)(p.q[q] + tile * 1024) + lane;
+                w[q][i] = NTL ? __builtin_nontemporal_load(src) : *src;
+                s[q][i] = p.s[q][tile * 64 + lane];
             }
-        // the last tile may end after two blocks: the others' values are 0
-        const bool in = kt * 128 + 32 * g < p.Kd;
+    }
+    // Step st (8 of each lane's 32 contraction values) as bf16.
+    __device__ __forceinline__ bf16x8 step(int q, int i, int st) const {
+        const float f = __uint_as_float(s[q][i] << 23);
+        const uint32_t d = w[q][i][st];
+        const u32x4 v = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, f, 0)),
+                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, f, 1)),
+                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, f, 2)),
+                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, f, 3))};
+        return __builtin_bit_cast(bf16x8, v);
+    }
+};
+
+// Columns n .. n+3 of row r, from the sums v (and u for gate/up).
+template <int MATS>
+__device__ __forceinline__ void store4(const Gemm4Params& p, int64_t r, int n, f32x4 v, f32x4 u) {
+    if (MATS == 2) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int i = 0; i < 4; ++i) v[i] = v[i] * __builtin_amdgcn_rcpf(1.0f + __expf(-v[i])) * u[i];
+    }
+    if (p.c) *(u32x2*)(p.c + r * p.N + n) = u32x2{pack_bf2x(v[0], v[1]), pack_bf2x(v[2], v[3])};
+    if (MATS == 1 && p.c32) *(f32x4*)(p.c32 + r * p.N + n) = v;
+}
+
+// 16 rows x 16*NT columns of a workgroup, the contraction tiles over its W waves.
+// Measured for one token (H = 4096, F = 1536, 8 experts): gate/up 11.7 us for
+// 53 MB of weights, down 7.4 us for 27 MB; gemm4_wide took 16.5 and 8.0.
+template <int MATS, int NT, int W>
+__global__ __launch_bounds__(64 * W) void gemm4_split(Gemm4Params p) {
+    constexpr int ACC = MATS * NT;
+    __shared__ f32x4 part[W][ACC][64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int slabs = (p.N / 16 + NT - 1) / NT;
+    int j, row0, rows, slab;
+    find_tile_of<16>(p, lane, slabs, j, row0, rows, slab);
+    if (j < 0) return;
+    const int nt0 = slab * NT, r16 = lane & 15, g = lane >> 4;
+
+    int64_t tiles[NT];
+    column_tiles(p, j, nt0, tiles);
+    struct Stage {
+        Weights4<MATS, NT> w;
+        u32x4 x[4];
+    } s0, s1;
+    int kt = wave;
+    // the first weights do not wait for the rows' indices
+    if (kt < p.KT) s0.w.template load<false>(p, tiles, kt, lane);
+    const auto rs = rows_rsrc(p, row0, rows);
+    uint32_t off = row_offset(p, row0, rows, r16);
+    if (off != kNoRow) off += 16u * g;
+    // load i: block i of the tile, 64 contiguous bytes of a row over the 4 lane
+    // groups (0 behind the contraction's end)
+    auto load_x = [&](Stage& t, int k) {
 #pragma unroll
-            for (int st = 0; st < 4; ++st)
-                t.x[m][st] = __builtin_bit_cast(
-                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                               rs, (in ? off[m] : kNoRow) + (uint32_t)(kt * 256 + st * 16), 0, 0));
+        for (int i = 0; i < 4; ++i)
+            t.x[i] = __builtin_bit_cast(
+                u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                           rs, (k * 128 + 32 * i < p.Kd ? off : kNoRow) + (uint32_t)(k * 256 + i * 64), 0, 0));
     };
-    f32x4 acc[MATS][NT][MT];
+    auto load = [&](Stage& t, int k) {
+        t.w.template load<false>(p, tiles, k, lane);
+        load_x(t, k);
+    };
+    f32x4 acc[MATS][NT];
 #pragma unroll
     for (int q = 0; q < MATS; ++q)
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int m = 0; m < MT; ++m) acc[q][i][m] = f32x4{};
-    auto multiply = [&](const Stage& t) {
+        for (int i = 0; i < NT; ++i) acc[q][i] = f32x4{};
+    auto multiply = [&](Stage& t) {
+        transpose4(t.x);
 #pragma unroll
         for (int q = 0; q < MATS; ++q)
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const float f = __uint_as_float(t.s[q][i] << 23);
+            for (int i = 0; i < NT; ++i)
 #pragma unroll
-                for (int st = 0; st < 4; ++st) {
-                    const uint32_t d = t.w[q][i][st];
-                    const u32x4 v = {
-                        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, f, 0)),
-                        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, f, 1)),
-                        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, f, 2)),
-                        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, f, 3))};
-                    const bf16x8 wv = __builtin_bit_cast(bf16x8, v);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-                        acc[q][i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            wv, __builtin_bit_cast(bf16x8, t.x[m][st]), acc[q][i][m], 0, 0, 0);
-                }
-            }
+                for (int st = 0; st < 4; ++st)
+                    acc[q][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        t.w.step(q, i, st), __builtin_bit_cast(bf16x8, t.x[st]), acc[q][i], 0, 0, 0);
     };
-    Stage s0, s1;
-    int kt = wave;
-    if (kt < p.KT) load(s0, kt);
+    if (kt < p.KT) load_x(s0, kt);
     for (; kt < p.KT; kt += 2 * W) {
         if (kt + W < p.KT) load(s1, kt + W);
         multiply(s0);
@@ -189,50 +255,204 @@ __global__ __launch_bounds__(64 * W) void gemm4_kernel(Gemm4Params p) {
         multiply(s1);
     }
 
-    // ---- the waves' sums, in wave order ----
+    // the waves' sums, in wave order
+#pragma unroll
+    for (int q = 0; q < MATS; ++q)
+#pragma unroll
+        for (int i = 0; i < NT; ++i) part[wave][q * NT + i][lane] = acc[q][i];
+    __syncthreads();
+    for (int t = wave; t < NT; t += W) {
+        f32x4 v[MATS];
+#pragma unroll
+        for (int q = 0; q < MATS; ++q) {
+            v[q] = part[0][q * NT + t][lane];
+#pragma unroll
+            for (int w = 1; w < W; ++w) v[q] += part[w][q * NT + t][lane];
+        }
+        // lane: row l%16, columns 4*(l/16) .. +3 of the 16 x 16 block
+        const int n = 16 * (nt0 + t) + 4 * g;
+        if (r16 < rows && n < p.N) store4<MATS>(p, (int64_t)row0 + r16, n, v[0], v[MATS - 1]);
+    }
+}
+
+// 16*MT rows x 64*NT columns of a workgroup of four waves.  A contraction tile of
+// the rows is [16*MT][128] bf16 in LDS, 256-byte rows with their 16-byte chunks
+// XOR-swizzled by row; two such buffers and one barrier a tile (a wave that
+// writes buffer b for tile k+2 has passed the barrier of tile k+1, which every
+// wave reaches after its reads of tile k).  Rows and weights of the next
+// tile are in flight while one is multiplied; deeper prefetch of the weights
+// (3 and 4 tiles) cost registers, and with them waves, and ran slower.
+// NTL: the weights carry the non-temporal hint (see launch4_rows).
+template <int MATS, int MT, int NT, bool NTL>
+__global__ __launch_bounds__(256) void gemm4_wide(Gemm4Params p) {
+    constexpr int W = 4;
+    __shared__ __attribute__((aligned(16))) uint8_t xs[2][MT * 4096];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int slabs = (p.N / 16 + NT * W - 1) / (NT * W);
+    int j, row0, rows, slab;
+    find_tile_of<16 * MT>(p, lane, slabs, j, row0, rows, slab);
+    if (j < 0) return;
+    const int nt0 = (slab * W + wave) * NT, r16 = lane & 15, g = lane >> 4;
+
+    int64_t tiles[NT];
+    column_tiles(p, j, nt0, tiles);
+    Weights4<MATS, NT> wb[2];
+    wb[0].template load<NTL>(p, tiles, 0, lane);  // does not wait for the rows' indices
+    const auto rs = rows_rsrc(p, row0, rows);
+    const int xrow = tid >> 4, xch = tid & 15;  // this thread's 16-byte chunk of rows xrow + 16*m
+    uint32_t off[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        off[m] = row_offset(p, row0, rows, 16 * m + xrow);
+        if (off[m] != kNoRow) off[m] += 16u * xch;
+    }
+    u32x4 xr[2][MT];
+    auto load_x = [&](u32x4 (&x)[MT], int kt) {
+        const bool in = kt * 128 + 8 * xch < p.Kd;  // 0 behind the contraction's end
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            x[m] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                 rs, (in ? off[m] : kNoRow) + (uint32_t)(kt * 256), 0, 0));
+    };
+    auto put_x = [&](const u32x4 (&x)[MT], int slot) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            *(MOE_LDS u32x4*)(xs[slot] + (16 * m + xrow) * 256 + ((xch ^ xrow) << 4)) = x[m];
+    };
+    f32x4 acc[MATS][NT][MT];
 #pragma unroll
     for (int q = 0; q < MATS; ++q)
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int m = 0; m < MT; ++m) part[wave][(q * NT + i) * MT + m][lane] = acc[q][i][m];
-    __syncthreads();
-    for (int t = wave; t < NT * MT; t += W) {
-        f32x4 v = part[0][t][lane];
+            for (int m = 0; m < MT; ++m) acc[q][i][m] = f32x4{};
+    auto multiply = [&](const Weights4<MATS, NT>& w, int slot) {
 #pragma unroll
-        for (int w = 1; w < W; ++w) v += part[w][t][lane];
-        if (MATS == 2) {
-            f32x4 u = part[0][ACC / 2 + t][lane];
+        for (int st = 0; st < 4; ++st) {
+            bf16x8 xf[MT];
 #pragma unroll
-            for (int w = 1; w < W; ++w) u += part[w][ACC / 2 + t][lane];
+            for (int m = 0; m < MT; ++m)
+                xf[m] = __builtin_bit_cast(
+                    bf16x8, *(const MOE_LDS u32x4*)(xs[slot] + (16 * m + r16) * 256 + (((4 * g + st) ^ r16) << 4)));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = v[i] * __builtin_amdgcn_rcpf(1.0f + __expf(-v[i])) * u[i];
+            for (int q = 0; q < MATS; ++q)
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const bf16x8 wv = w.step(q, i, st);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+                        acc[q][i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, xf[m], acc[q][i][m], 0, 0, 0);
+                }
         }
-        // lane: row l%16, columns 4*(l/16) .. +3 of the 16 x 16 block
-        const int r = 16 * (t % MT) + r16;
-        const int n = 16 * (nt0 + t / MT) + 4 * g;
-        if (r < rows && n < p.N)
-            *(u32x2*)(p.c + (int64_t)(row0 + r) * p.N + n) = u32x2{pack_bf2x(v[0], v[1]), pack_bf2x(v[2], v[3])};
+    };
+    load_x(xr[0], 0);
+    for (int k0 = 0; k0 < p.KT; k0 += 2) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int kt = k0 + u;
+            if (kt >= p.KT) break;
+            put_x(xr[u], u);
+            if (kt + 1 < p.KT) {
+                load_x(xr[u ^ 1], kt + 1);
+                wb[u ^ 1].template load<NTL>(p, tiles, kt + 1, lane);
+            }
+            __syncthreads();
+            multiply(wb[u], u);
+        }
     }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int r = 16 * m + r16, n = 16 * (nt0 + i) + 4 * g;
+            if (r < rows && n < p.N)
+                store4<MATS>(p, (int64_t)row0 + r, n, acc[0][i][m], acc[MATS - 1][i][m]);
+        }
 }
 
-template <int MATS, int MT, int NT, int W>
-static int launch4(const Gemm4Params& p, hipStream_t s) {
-    const int64_t bm = 16 * MT;
-    const int64_t tiles = std::min<int64_t>(p.cap, p.cap / bm + p.e_local);
-    const int64_t slabs = (p.N / 16 + NT - 1) / NT;
-    const int64_t grid = (tiles * slabs + 7) / 8 * 8;
+template <int MATS, int NT, int W>
+static int launch_split(const Gemm4Params& p, hipStream_t s) {
+    const int64_t tiles = std::min<int64_t>(p.cap, p.cap / 16 + p.e_local);
+    const int64_t grid = (tiles * ((p.N / 16 + NT - 1) / NT) + 7) / 8 * 8;
     if (grid >= (1ll << 31)) return MOE_EINVAL;
-    gemm4_kernel<MATS, MT, NT, W><<<(unsigned)grid, 64 * W, 0, s>>>(p);
+    gemm4_split<MATS, NT, W><<<(unsigned)grid, 64 * W, 0, s>>>(p);
     return moe_host::launch_status();
 }
 
+template <int MATS, int MT, int NT, bool NTL>
+static int launch_wide(const Gemm4Params& p, hipStream_t s) {
+    const int64_t tiles = std::min<int64_t>(p.cap, p.cap / (16 * MT) + p.e_local);
+    const int64_t grid = (tiles * ((p.N / 16 + NT * 4 - 1) / (NT * 4)) + 7) / 8 * 8;
+    if (grid >= (1ll << 31)) return MOE_EINVAL;
+    gemm4_wide<MATS, MT, NT, NTL><<<(unsigned)grid, 256, 0, s>>>(p);
+    return moe_host::launch_status();
+}
+
+// Which kernel, from the host's sizes alone: cap rows over e_local experts make at
+// most `tiles` row tiles of 16.
+//   split: fewer than 3 waves a SIMD (3072) if every wave took 16 columns.
+//     One token, H = 4096, F = 1536, gate/up (768): 11.7 us against 16.5 us;
+//     four tokens (3072): 36.8 against 34.4.  Down, one token (2048): 7.4 against
+//     8.0; two (4096): 11.9 against 10.7.  Two column tiles a workgroup once those
+//     make 512 workgroups, two a CU (gate/up of two tokens 19.9 against 22.9 us, of
+//     one 12.8 against 11.7).
+//   wide: row tiles of 16, or of 32 when there are more than 16 rows an expert
+//     (gate/up of 512 tokens, 128 experts: 183 against 207 us; 64 rows were slower
+//     at every size, the accumulators leaving too few waves).
+//   non-temporal weights: when the packed matrices that the rows can touch
+//     fill half the last-level cache (128 MB) or more, so that they are not there the
+//     next time, and an expert's rows mostly fit one tile (three quarters of it or
+//     less on average), so that no other workgroup reads them again.  Gate/up of 256
+//     tokens on 32 experts 82 against 90 us; of 512 on 128 experts, whose larger ones
+//     take three tiles, 190 against 183.
 template <int MATS>
 static int launch4_rows(const Gemm4Params& p, hipStream_t s) {
-    const int64_t avg = (p.cap + p.e_local - 1) / p.e_local;
-    if (avg <= 16) return launch4<MATS, 1, 2, 8>(p, s);
-    if (avg <= 32) return launch4<MATS, 2, 2, 4>(p, s);
-    return launch4<MATS, 4, 2, 4>(p, s);
+    const int64_t cols = p.N / 16;
+    const int64_t tiles = std::min<int64_t>(p.cap, p.cap / 16 + p.e_local);
+    if (tiles * cols < 3072) {
+        if (tiles * cols >= 1024) return launch_split<MATS, 2, 4>(p, s);
+        return launch_split<MATS, 1, 4>(p, s);
+    }
+    const int64_t experts = std::min<int64_t>(p.cap, p.e_local);
+    const bool large = experts * MATS * p.N * p.Kd * 17 / 32 >= (128ll << 20);
+    if (p.cap <= 16ll * p.e_local) {
+        if (large && p.cap <= 12ll * p.e_local) return launch_wide<MATS, 1, 2 / MATS, true>(p, s);
+        return launch_wide<MATS, 1, 2 / MATS, false>(p, s);
+    }
+    if (p.cap <= 24ll * p.e_local) {
+        if (large) return launch_wide<MATS, 2, 2, true>(p, s);
+        return launch_wide<MATS, 2, 2, false>(p, s);
+    }
+    // several row tiles an expert: down takes 256 columns a workgroup, reading the rows half as often
+    // (512 tokens: 110 against 125 us; gate/up has no registers left for it)
+    return launch_wide<MATS, 2, 4 / MATS, false>(p, s);
+}
+
+// out[t] = bf16(sum over k ascending of gate[t,k] * y[pos[t,k]]) from fp32 rows: moe_combine without the rounding
+// of y.  4 columns per thread; a token's rows and gates are the same in every lane of a wave.
+__global__ __launch_bounds__(256) void combine32_kernel(const float* __restrict__ y, int64_t cap,
+                                                        const int32_t* __restrict__ pos,
+                                                        const float* __restrict__ gates, int T, int K, int N,
+                                                        uint16_t* __restrict__ out) {
+    const int n = (int)(blockIdx.x * 64 + (threadIdx.x & 63)) * 4;
+    const int64_t t = (int64_t)blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (t >= T || n >= N) return;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k0 = 0; k0 < K; k0 += 8) {
+        f32x4 v[8];
+        float g[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = k0 + k < K ? pos[t * K + k0 + k] : -1;
+            const bool in = r >= 0 && r < cap;
+            v[k] = in ? *(const f32x4*)(y + (int64_t)r * N + n) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            g[k] = in ? gates[t * K + k0 + k] : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc += g[k] * v[k];
+    }
+    *(u32x2*)(out + t * N + n) = u32x2{pack_bf2x(acc[0], acc[1]), pack_bf2x(acc[2], acc[3])};
 }
 
 // Checks common to both products; MOE_OK with *nothing set: no work.
@@ -312,4 +532,51 @@ extern "C" int moe_grouped_gemm4(const moe_bf16* a, const uint8_t* q4, const uin
     p.KT = (Kd + 127) / 128;
     p.c = c;
     return launch4_rows<1>(p, (hipStream_t)stream);
+}
+
+extern "C" size_t moe_gemm4_combine_workspace_size(int cap_rows, int N) {
+    return cap_rows > 0 && N > 0 ? (size_t)cap_rows * (size_t)N * 4 : 0;
+}
+
+extern "C" int moe_grouped_gemm4_combine(const moe_bf16* a, const uint8_t* q4, const uint8_t* s4,
+                                         const int32_t* offsets, int e_local, int Kd, int N, int cap_rows,
+                                         const int32_t* pos, const float* gates, int T, int K, moe_bf16* y,
+                                         moe_bf16* out, void* ws, size_t ws_bytes, moe_stream stream) {
+    using namespace moe;
+    bool nothing;
+    const int rc = check_gemm4(e_local, Kd, N, cap_rows, offsets, &nothing);
+    if (rc != MOE_OK) return rc;
+    if (T < 0 || K < 1 || K > 16 || (int64_t)T * K >= (1ll << 31)) return MOE_EINVAL;
+    if (T > 4 * 65535) return MOE_EINVAL;
+    if (T == 0 || N == 0) return MOE_OK;
+    if (!pos || !gates || !out) return MOE_EINVAL;
+    if (!nothing && (!a || !q4 || !s4)) return MOE_EINVAL;
+    if (misaligned(a) || misaligned(q4) || misaligned(s4) || misaligned(offsets) || misaligned(pos) ||
+        misaligned(gates) || misaligned(y) || misaligned(out) || misaligned(ws))
+        return MOE_EALIGN;
+    if (!nothing && (!ws || ws_bytes < moe_gemm4_combine_workspace_size(cap_rows, N))) return MOE_EWORKSPACE;
+    hipStream_t s = (hipStream_t)stream;
+    if (!nothing) {
+        Gemm4Params p{};
+        p.a = a;
+        p.topk = 1;
+        p.topk_rcp = 0xffffffffu;
+        p.a_rows = cap_rows;
+        p.q[0] = q4;
+        p.s[0] = s4;
+        p.offsets = offsets;
+        p.e_local = e_local;
+        p.cap = cap_rows;
+        p.Kd = Kd;
+        p.N = N;
+        p.KT = (Kd + 127) / 128;
+        p.c = y;
+        p.c32 = (float*)ws;
+        const int st = launch4_rows<1>(p, s);
+        if (st != MOE_OK) return st;
+    }
+    // with no expert or no row here, every token's sum is empty: cap 0 takes no row
+    combine32_kernel<<<dim3((N / 4 + 63) / 64, (T + 3) / 4), 256, 0, s>>>((const float*)ws, nothing ? 0 : cap_rows,
+                                                                          pos, gates, T, K, N, out);
+    return moe_host::launch_status();
 }

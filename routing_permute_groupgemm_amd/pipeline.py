@@ -28,7 +28,7 @@ class MoeBuffers:
     ws: torch.Tensor
     h: torch.Tensor
     ab: torch.Tensor | None
-    y: torch.Tensor
+    y: torch.Tensor | None  # None with weights4
     out: torch.Tensor
     # backward
     dy_perm: torch.Tensor | None = None
@@ -46,13 +46,18 @@ class MoeBuffers:
     # 8-bit checkpoint: the forward saves (a, b) in 8-bit blocks instead of ab, and the backward recomputes
     # h from them, so h is scratch that layers may share
     checkpoint8: bool = False
+    # 4-bit weights (forward4): the experts' rows stay in fp32 in ws4, there is no y
+    weights4: bool = False
+    ws4: torch.Tensor | None = None
     ab8: torch.Tensor | None = None
     ab8_scale: torch.Tensor | None = None
 
     @classmethod
     def allocate(cls, shape: MoeShape, cap: int | None = None, device="cuda", backward=None, zero_copy=False,
-                 checkpoint8=False):
+                 checkpoint8=False, weights4=False):
         backward = shape.backward if backward is None else backward
+        if weights4:  # serving: the products read the tokens through src
+            backward, zero_copy = False, True
         T, H, F, K, EL = shape.T, shape.H, shape.F, shape.K, shape.EL
         cap = shape.cap if cap is None else cap
         capn = max(cap, 1)
@@ -64,8 +69,11 @@ class MoeBuffers:
                 pos=e((T, K), dt=torch.int32), src=e(capn, dt=torch.int32),
                 x_perm=None if zero_copy else e((capn, H)),
                 status=e(4, dt=torch.int32), ws=e(ws_bytes, dt=torch.uint8), h=e((capn, F)),
-                ab=e((capn, 2 * F)) if backward and not checkpoint8 else None, y=e((capn, H)), out=e((T, H)),
-                zero_copy=zero_copy, checkpoint8=checkpoint8 and backward)
+                ab=e((capn, 2 * F)) if backward and not checkpoint8 else None,
+                y=None if weights4 else e((capn, H)), out=e((T, H)), zero_copy=zero_copy,
+                checkpoint8=checkpoint8 and backward, weights4=weights4)
+        if weights4:
+            b.ws4 = e(max(_lib.moe_gemm4_combine_workspace_size(cap, H), 256), dt=torch.uint8)
         if b.checkpoint8:
             b.ab8 = e((capn, 2 * F), dt=torch.int8)
             b.ab8_scale = e((capn, 2 * F // 32), dt=torch.uint8)
@@ -135,15 +143,15 @@ def pack_weights4(inp: dict) -> dict:
 
 def forward4(buf: MoeBuffers, inp: dict):
     """The forward of a decode step on 4-bit weights. inp: device tensors logits and x, and pack_weights4's
-    pairs. The products read the tokens through src, so the buffers are zero-copy ones."""
+    pairs; buffers allocated with weights4=True."""
     s = buf.shape
-    if not buf.zero_copy:
-        raise _lib.MoeError("forward4: the buffers need zero_copy=True")
+    if not buf.weights4:
+        raise _lib.MoeError("forward4: the buffers need weights4=True")
     route(buf, inp["logits"])
     permute(buf, inp["x"])
     _lib.moe_grouped_gemm4_swiglu(inp["x"], buf.src, s.K, inp["w_gate4"], inp["w_up4"], buf.offsets, buf.cap, h=buf.h)
-    _lib.moe_grouped_gemm4(buf.h, inp["w_down4"], buf.offsets, buf.cap, c=buf.y)
-    combine(buf)
+    _lib.moe_grouped_gemm4_combine(buf.h, inp["w_down4"], buf.offsets, buf.cap, buf.pos, buf.gates, out=buf.out,
+                                   ws=buf.ws4)
     return buf.out
 
 

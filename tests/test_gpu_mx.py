@@ -321,6 +321,9 @@ def reference4(x, w, off):
 
 
 COUNTS = {
+    "wide_rows": [20] * 20,
+    "even": [13, 9, 11, 14] * 6,
+    "tens": [25, 60, 31, 40, 33, 28] * 2,
     "one_row": [1],
     "single_token": [0, 1, 0, 0, 1, 0, 1, 1],
     "ragged": [3, 0, 17, 16, 1, 33, 0, 15],
@@ -331,12 +334,26 @@ COUNTS = {
 }
 
 
-@pytest.mark.parametrize("H,F", [(64, 64), (128, 192), (192, 128), (320, 64), (1408, 320)])
+def check_combined(got, pos, gates, y, ey):
+    """sum_k gate * y over the present pairs: K roundings on top of the rows' own, and the last one to bf16."""
+    T, K = pos.shape
+    out, tol = np.zeros((T, y.shape[1])), np.zeros((T, y.shape[1]))
+    for k in range(K):
+        ok = pos[:, k] >= 0
+        g = gates[ok, k, None].astype(np.float64)
+        out[ok] += g * y[pos[ok, k]]
+        tol[ok] += g * (ey[pos[ok, k]] + 2 * K * U32 * np.abs(y[pos[ok, k]]))
+    within("out", got, out, tol + UBF * np.abs(out) + 1e-37)
+
+
+@pytest.mark.parametrize("H,F", [(64, 64), (128, 192), (192, 128), (320, 64), (1408, 320), (2112, 1984)])
 @pytest.mark.parametrize("counts", list(COUNTS))
 def test_gemm4_against_float64(counts, H, F):
     n = COUNTS[counts]
     if len(n) > 100 and H * F > 128 * 192:
         H, F = 64, 128
+    if H * F > 1408 * 320 and counts not in ("wide_rows", "even", "tens"):
+        H, F = 64, 1088
     K, R = 4, sum(n)
     T = max(R, 8)
     print(f"[mx] gemm4 {counts} H={H} F={F} R={R}", flush=True)
@@ -374,6 +391,48 @@ def test_gemm4_against_float64(counts, H, F):
     wy, ey = reference4(mx_ref.f64(bits(h))[:R], vals["down"], off)
     within("y", bits(y)[:R], wy, ey + UBF * np.abs(wy) + 1e-37)
     assert (y[R:] == 5.0).all()
+    # down and combine in one: the same y, and the gated sum of the unrounded rows (absent pairs -1)
+    pos = np.full(T * K, -1, np.int32)
+    pos[src] = np.arange(R)
+    gates = np.random.default_rng(37).random((T, K)).astype(np.float32)
+    y2 = torch.full((cap, H), 5.0, dtype=torch.bfloat16, device="cuda")
+    args = (hin, packed["down"], offsets, cap, torch.from_numpy(pos.reshape(T, K)).cuda(), torch.from_numpy(gates).cuda())
+    out = _lib.moe_grouped_gemm4_combine(*args, y=y2)
+    assert_equal("y of the combined call", bits(y2), bits(y))
+    check_combined(bits(out), pos.reshape(T, K), gates, wy, ey)
+    assert_equal("without y", bits(_lib.moe_grouped_gemm4_combine(*args)), bits(out))
+
+
+@pytest.mark.parametrize("rows", [3, 9, 20, 40])
+def test_gemm4_large_matrices(rows):
+    """Matrices past half the last-level cache (the non-temporal loads) at every row tile: 40 experts of about
+    `rows` rows, one of them with three times as many and one with none, against float64 on the GPU."""
+    E, Kd, N = 40, 4096, 2112
+    rng = np.random.default_rng(rows)
+    n = rng.integers(max(rows - 3, 1), rows + 2, E)
+    n[7], n[11] = 3 * rows, 0
+    off = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+    R = int(off[-1])
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(rows)
+    mats = [(torch.randn((E, Kd, N), generator=gen, device="cuda") * 0.02).to(torch.bfloat16) for _ in range(2)]
+    x = torch.randn((R, Kd), generator=gen, device="cuda").to(torch.bfloat16)
+    packed = [_lib.moe_pack4(m) for m in mats]
+    offsets = torch.from_numpy(off).cuda()
+    print(f"[mx] gemm4 large, {R} rows", flush=True)
+    c = _lib.moe_grouped_gemm4(x, packed[0], offsets, R)
+    h = _lib.moe_grouped_gemm4_swiglu(x, None, None, packed[0], packed[1], offsets, R)
+    vals = [_lib.moe_unpack4(*p, Kd) for p in packed]
+    for j in range(E):
+        lo, hi = off[j], off[j + 1]
+        xr = x[lo:hi].double()
+        a, b = (xr @ v[j].double() for v in vals)
+        ea, eb = (Kd * U32 * (xr.abs() @ v[j].double().abs()) for v in vals)
+        assert ((c[lo:hi].double() - a).abs() <= ea + UBF * a.abs()).all(), j
+        sg = torch.sigmoid(a)
+        want = a * sg * b
+        tol = 1.1 * ea * b.abs() + (a * sg).abs() * eb + 1.1 * ea * eb + (UBF + 2.0 ** -18) * want.abs() + 1e-37
+        assert ((h[lo:hi].double() - want).abs() <= tol).all(), j
 
 
 @pytest.mark.parametrize("counts", ["ragged", "many"])
@@ -480,38 +539,31 @@ def test_training_step_with_8bit_checkpoint(name, zero_copy):
 @pytest.mark.parametrize("T", [1, 2, 37, 300])
 @pytest.mark.parametrize("name", ["tiny", "ep_share_small", "skew_small"])
 def test_decode_step_on_4bit_weights(name, T):
-    """forward4 against the bf16 forward on the unpacked weights: h and y each differ by their roundings."""
+    """forward4 from routing to output; the routing is the bf16 forward's."""
     shape = SHAPES[name].scaled(T=T)
     inp = synth.make_inputs(shape, seed=41)
     dev = pipeline.to_device(inp)
     dev.update(pipeline.pack_weights4(dev))
     ref = pipeline.MoeBuffers.allocate(shape, zero_copy=True, backward=False)
-    buf = pipeline.MoeBuffers.allocate(shape, zero_copy=True, backward=False)
-    plain = dict(dev)
-    for k, kd in (("w_gate", shape.H), ("w_up", shape.H), ("w_down", shape.F)):
-        plain[k] = _lib.moe_unpack4(*dev[k + "4"], kd)
+    buf = pipeline.MoeBuffers.allocate(shape, weights4=True)
+    assert buf.y is None and buf.zero_copy
     pipeline.forward4(buf, dev)
-    pipeline.forward(ref, plain)
+    pipeline.forward(ref, dev)
+    assert_equal("routing", bits(buf.pos), bits(ref.pos))
     R = min(int(buf.offsets[-1].item()), buf.cap)
-    h, y = mx_ref.f64(bits(buf.h))[:R], mx_ref.f64(bits(buf.y))[:R]
-    # two fp32 sums of the same products and two bf16 roundings
-    off = np.minimum(bits(buf.offsets), R)
+    h, off = mx_ref.f64(bits(buf.h)[:R]), np.minimum(bits(buf.offsets), R)
+    w = {k: mx_ref.f64(bits(_lib.moe_unpack4(*dev[k + "4"], kd)))
+         for k, kd in (("w_gate", shape.H), ("w_up", shape.H), ("w_down", shape.F))}
     xr = mx_ref.f64(inp["x"])[bits(buf.src)[:R] // shape.K]
-    a, ea = reference4(xr, mx_ref.f64(bits(plain["w_gate"])), off)
-    b, eb = reference4(xr, mx_ref.f64(bits(plain["w_up"])), off)
+    a, ea = reference4(xr, w["w_gate"], off)
+    b, eb = reference4(xr, w["w_up"], off)
     sg = 1 / (1 + np.exp(-a))
     within("h", h, a * sg * b, 1.1 * ea * np.abs(b) + np.abs(a * sg) * eb + 1.1 * ea * eb
            + (UBF + 2.0 ** -18) * np.abs(a * sg * b) + 1e-37)
-    wy, ey = reference4(h, mx_ref.f64(bits(plain["w_down"])), off)
-    within("y", y, wy, ey + UBF * np.abs(wy) + 1e-37)
-    out, pos, g = np.zeros((T, shape.H)), bits(buf.pos), bits(buf.gates).astype(np.float64)
-    mag = np.zeros_like(out)
-    for k in range(shape.K):
-        ok = pos[:, k] >= 0
-        out[ok] += g[ok, k, None] * y[pos[ok, k]]
-        mag[ok] += np.abs(g[ok, k, None] * y[pos[ok, k]])
-    within("out", bits(buf.out), out, UBF * np.abs(out) + 32 * U32 * mag + 1e-37)
-    assert_equal("routing", bits(buf.pos), bits(ref.pos))
+    y, ey = reference4(h, w["w_down"], off)
+    check_combined(bits(buf.out), bits(buf.pos), bits(buf.gates), y, ey)
+    with pytest.raises(_lib.MoeError):
+        pipeline.forward4(ref, dev)
 
 
 def test_replay_from_a_graph_and_another_stream():
@@ -521,7 +573,7 @@ def test_replay_from_a_graph_and_another_stream():
     dev = pipeline.to_device(inp)
     dev.update(pipeline.pack_weights4(dev))
     train = pipeline.MoeBuffers.allocate(shape, checkpoint8=True)
-    serve = pipeline.MoeBuffers.allocate(shape, zero_copy=True, backward=False)
+    serve = pipeline.MoeBuffers.allocate(shape.scaled(backward=False), weights4=True)
 
     def step():
         pipeline.forward(train, dev)
@@ -545,7 +597,7 @@ def test_replay_from_a_graph_and_another_stream():
     with torch.cuda.graph(graph):
         step()
     for _ in range(3):
-        for t in outs + [train.h, serve.h, serve.y]:
+        for t in outs + [train.h, serve.h, serve.ws4]:
             t.fill_(7)
         torch.cuda.synchronize()
         graph.replay()

@@ -152,6 +152,27 @@ def test_gemm4_refusals():
     assert d(FAKE, FAKE, FAKE, FAKE, 4, 64, 64, -1, FAKE, None) == -1
 
 
+def test_gemm4_combine_refusals():
+    lib = _lib.load()
+    assert lib.moe_gemm4_combine_workspace_size(10, 64) == 2560
+    assert lib.moe_gemm4_combine_workspace_size(0, 64) == 0 and lib.moe_gemm4_combine_workspace_size(-1, 64) == 0
+    names = ("a", "q4", "s4", "off", "el", "Kd", "N", "cap", "pos", "gates", "T", "K", "y", "out", "ws", "wsb", "st")
+    ok = (FAKE, FAKE, FAKE, FAKE, 4, 64, 64, 16, FAKE, FAKE, 8, 2, None, FAKE, FAKE, 1 << 20, None)
+
+    def call(**kw):
+        a = dict(zip(names, ok), **kw)
+        return lib.moe_grouped_gemm4_combine(*(a[n] for n in names))
+
+    assert call(Kd=96) == -2 and call(N=96) == -2
+    assert call(K=0) == -1 and call(K=17) == -1 and call(T=-1) == -1 and call(T=262141) == -1
+    for n in ("a", "q4", "s4", "off", "pos", "gates", "out"):
+        assert call(**{n: None}) == -1, n
+    for n in ("a", "q4", "s4", "off", "pos", "gates", "y", "out", "ws"):
+        assert call(**{n: MIS}) == -3, n
+    assert call(ws=None) == -4 and call(wsb=16 * 64 * 4 - 1) == -4
+    assert call(T=0, pos=None) == 0
+
+
 def test_binding_refuses_host_tensors_and_wrong_types():
     x = torch.zeros((4, 64), dtype=torch.bfloat16)
     with pytest.raises(_lib.MoeError):
