@@ -314,8 +314,8 @@ def _own(st):
                                           dab=st["dab"], h=st["h"])
         return {"dab": st["dab"], "h": st["h"]}
     _lib.moe_grouped_gemm4_swiglu(st["x"], p["src"], case["K"], st["gate"], st["up"], p["offsets"], cap, h=st["h"])
-    _lib.moe_grouped_gemm4(st["h"], st["down"], p["offsets"], cap, c=st["y"])
-    _lib.moe_combine(st["y"], p["pos"], p["gates"], out=st["out"])
+    _lib.moe_grouped_gemm4_combine(st["h"], st["down"], p["offsets"], cap, p["pos"], p["gates"], y=st["y"],
+                                   out=st["out"])
     return {"h": st["h"], "y": st["y"], "out": st["out"]}
 
 
