@@ -91,10 +91,27 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# the current stream's handle without a Stream object around it (2.5 us less per call), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
+
+
+def _on_device(stream, *tensors):
+    """The stream's handle, after checking that it and every tensor are on the current device."""
+    dev = torch.cuda.current_device()
+    if stream is not None and stream.device_index != dev:
+        raise MoeError(f"a stream of device {stream.device_index} with device {dev} current")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise MoeError(f"a tensor on {t.device} with device {dev} current")
+    return _stream(stream)
 
 
 def _need(t, dtype, name):
@@ -557,7 +574,7 @@ def moe_pack8(x, q=None, scale=None, offsets=None, stream=None):
     rows, cols = x.shape
     q, scale = _save8(q, scale, rows, cols, x.device)
     _check(load().moe_pack8(_ptr(x), rows, cols, _ptr(offsets), _routed(offsets), _ptr(q), _ptr(scale),
-                            _stream(stream)))
+                            _on_device(stream, x, offsets, q, scale)))
     return q, scale
 
 
@@ -574,7 +591,7 @@ def moe_unpack8(q, scale, x=None, offsets=None, stream=None):
     _need(x, torch.bfloat16, "x")
     _rows(x, rows, cols, "x")
     _check(load().moe_unpack8(_ptr(q), _ptr(scale), rows, cols, _ptr(offsets), _routed(offsets), _ptr(x),
-                              _stream(stream)))
+                              _on_device(stream, q, scale, offsets, x)))
     return x
 
 
@@ -592,7 +609,8 @@ def moe_grouped_gemm_swiglu_save8(x_perm, w_gate, w_up, offsets, cap_rows, h=Non
     ab8, ab8_scale = _save8(ab8, ab8_scale, max(cap_rows, 0), 2 * F, x_perm.device, ("ab8", "ab8_scale"))
     _rows(x_perm, cap_rows, H, "x_perm")
     _check(load().moe_grouped_gemm_swiglu_save8(_ptr(x_perm), _ptr(w_gate), _ptr(w_up), _ptr(offsets), EL, H, F,
-                                                cap_rows, _ptr(h), _ptr(ab8), _ptr(ab8_scale), _stream(stream)))
+                                                cap_rows, _ptr(h), _ptr(ab8), _ptr(ab8_scale),
+                                                _on_device(stream, x_perm, w_gate, w_up, offsets, h, ab8, ab8_scale)))
     return h, ab8, ab8_scale
 
 
@@ -615,7 +633,9 @@ def moe_grouped_gemm_swiglu_gather_save8(x, src, K, w_gate, w_up, offsets, cap_r
         raise MoeError(f"src: expected at least {cap_rows} entries, got {src.numel()}")
     _check(load().moe_grouped_gemm_swiglu_gather_save8(_ptr(x), T, _ptr(src), int(K), _ptr(w_gate), _ptr(w_up),
                                                        _ptr(offsets), EL, H, F, cap_rows, _ptr(h), _ptr(ab8),
-                                                       _ptr(ab8_scale), _stream(stream)))
+                                                       _ptr(ab8_scale),
+                                                       _on_device(stream, x, src, w_gate, w_up, offsets, h, ab8,
+                                                                  ab8_scale)))
     return h, ab8, ab8_scale
 
 
@@ -644,7 +664,8 @@ def moe_grouped_gemm_swiglu_bwd8(dy_perm, w_down, offsets, cap_rows, ab8, ab8_sc
         _need(h, torch.bfloat16, "h")
         _rows(h, cap_rows, F, "h")
     _check(load().moe_grouped_gemm_swiglu_bwd8(_ptr(dy_perm), _ptr(w_down), _ptr(offsets), EL, H, F, cap_rows,
-                                               _ptr(ab8), _ptr(ab8_scale), _ptr(dab), _ptr(h), _stream(stream)))
+                                               _ptr(ab8), _ptr(ab8_scale), _ptr(dab), _ptr(h),
+                                               _on_device(stream, dy_perm, w_down, offsets, ab8, ab8_scale, dab, h)))
     return dab, h
 
 
@@ -683,7 +704,7 @@ def moe_pack4(w, q4=None, s4=None, stream=None):
     if s4 is None:
         s4 = torch.empty(shapes[1], dtype=torch.uint8, device=w.device)
     _weights4((q4, s4), Kd, "w", E, N)
-    _check(load().moe_pack4(_ptr(w), E, Kd, N, _ptr(q4), _ptr(s4), _stream(stream)))
+    _check(load().moe_pack4(_ptr(w), E, Kd, N, _ptr(q4), _ptr(s4), _on_device(stream, w, q4, s4)))
     return q4, s4
 
 
@@ -694,7 +715,7 @@ def moe_unpack4(q4, s4, Kd, w=None, stream=None):
         w = torch.empty((E, Kd, N), dtype=torch.bfloat16, device=q4.device)
     _need(w, torch.bfloat16, "w")
     _shape(w, (E, Kd, N), "w")
-    _check(load().moe_unpack4(_ptr(q4), _ptr(s4), E, Kd, N, _ptr(w), _stream(stream)))
+    _check(load().moe_unpack4(_ptr(q4), _ptr(s4), E, Kd, N, _ptr(w), _on_device(stream, q4, s4, w)))
     return w
 
 
@@ -721,7 +742,8 @@ def moe_grouped_gemm4_swiglu(x, src, K, gate, up, offsets, cap_rows, h=None, str
     _need(h, torch.bfloat16, "h")
     _rows(h, cap_rows, F, "h")
     _check(load().moe_grouped_gemm4_swiglu(_ptr(x), T, _ptr(src), int(K or 0), _ptr(gq), _ptr(gs), _ptr(uq),
-                                           _ptr(us), _ptr(offsets), EL, H, F, cap_rows, _ptr(h), _stream(stream)))
+                                           _ptr(us), _ptr(offsets), EL, H, F, cap_rows, _ptr(h),
+                                           _on_device(stream, x, src, gq, gs, uq, us, offsets, h)))
     return h
 
 
@@ -740,7 +762,7 @@ def moe_grouped_gemm4(a, w, offsets, cap_rows, c=None, stream=None):
     _need(c, torch.bfloat16, "c")
     _rows(c, cap_rows, N, "c")
     _check(load().moe_grouped_gemm4(_ptr(a), _ptr(q4), _ptr(s4), _ptr(offsets), EL, Kd, N, cap_rows, _ptr(c),
-                                    _stream(stream)))
+                                    _on_device(stream, a, q4, s4, offsets, c)))
     return c
 
 
@@ -778,7 +800,7 @@ def moe_grouped_gemm4_combine(a, w, offsets, cap_rows, pos, gates, y=None, out=N
     _need(ws, torch.uint8, "ws")
     _check(load().moe_grouped_gemm4_combine(_ptr(a), _ptr(q4), _ptr(s4), _ptr(offsets), EL, Kd, N, cap_rows,
                                             _ptr(pos), _ptr(gates), T, K, _ptr(y), _ptr(out), _ptr(ws), ws.numel(),
-                                            _stream(stream)))
+                                            _on_device(stream, a, q4, s4, offsets, pos, gates, y, out, ws)))
     return out
 
 

@@ -1025,7 +1025,128 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
             constexpr bool kBwd8 = EPI == EPI_SWIGLU_BWD8;
             static_assert(EPI == EPI_SWIGLU_BWD || kBwd8 || SCHED == SCHED_WGRAD,
                           "16x16x32 body: the down dgrad or dW");
-            if constexpr (kBwd8 || (EPI == EPI_SWIGLU_BWD && MOE_GEMM_DGRAD_STAGED)) {  // the accumulators are dh
+            if constexpr (kBwd8) {  // the accumulators are dh
+                // The bf16 form below with the saved bytes staged instead of their bf16
+                // values: a 16-row block is 128 bytes a row of a and of b (16 bytes per
+                // lane, 8 rows per load) in the wave's first 4 KiB, 16-byte chunks
+                // XOR-swizzled by row pair.  Each lane reads the four bytes of its
+                // MFMA-layout columns and widens them there, with the scales of its own
+                // row; (da, db) and then h go out as whole 256-byte row pieces through the
+                // same 8 KiB.
+                static_assert(TL::kStage / TL::kWaves >= 8192 && BN / WN == 128, "staging space per wave");
+                uint8_t* stg = smem + ((gs + S - 1) % S) * TL::kStage + wave * 8192;
+                const int ln = lane_id_here();
+                auto sq = [&](int hb, int row, int chunk) {
+                    return (MOE_LDS uint8_t*)(stg + hb * 2048 + row * 128 + ((chunk ^ (row >> 1)) << 4));
+                };
+                auto sa = [&](int hb, int row, int chunk) {
+                    return (MOE_LDS uint8_t*)(stg + hb * 4096 + row * 256 + ((chunk ^ row) << 4));
+                };
+                const int r = ln & 15, q = ln >> 4;    // MFMA layout: row, columns 4q..4q+3 of each 16
+                const int rb = ln >> 3, cb = ln & 7;   // bytes in: load i covers rows 8i + rb, chunk cb
+                const int rw = ln >> 4, cc = ln & 15;  // rows out: store i covers rows 4i + rw, chunk cc
+                const int n0 = ni * BN + wn * (BN / WN);  // the wave's first column
+                constexpr int kPre = MOE_GEMM_DGRAD_PREFETCH;
+                u32x4 ld[kPre][2][2];
+                uint32_t sl[kPre][2], sh[kPre][2];  // scale bytes of columns n0..n0+63 and n0+64..n0+127
+                auto issue_loads = [&](int m) {
+                    const int k = m % kPre;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int mloc = row16(m) + 8 * i + rb;
+                        ld[k][0][i] = ld[k][1][i] = u32x4{0u, 0u, 0u, 0u};
+                        if (mloc < valid && n0 + 16 * cb < p.N) {
+                            const int8_t* src = p.q8 + (int64_t)(row0 + mloc) * 2 * p.N + n0 + 16 * cb;
+                            ld[k][0][i] = *(const u32x4*)src;
+                            ld[k][1][i] = *(const u32x4*)(src + p.N);
+                        }
+                    }
+                    sl[k][0] = sl[k][1] = sh[k][0] = sh[k][1] = 0u;
+                    if (row16(m) + r < valid && n0 < p.N) {
+                        const uint8_t* src = p.s8 + (((int64_t)(row0 + row16(m) + r) * 2 * p.N + n0) >> 5);
+                        const int up = p.N >> 5;
+                        sl[k][0] = *(const uint16_t*)src;
+                        sl[k][1] = *(const uint16_t*)(src + up);
+                        if (n0 + 64 < p.N) {
+                            sh[k][0] = *(const uint16_t*)(src + 2);
+                            sh[k][1] = *(const uint16_t*)(src + up + 2);
+                        }
+                    }
+                };
+#pragma unroll
+                for (int m = 0; m < kPre && m < MB16; ++m) issue_loads(m);
+#pragma unroll
+                for (int m = 0; m < MB16; ++m) {
+                    const int k = m % kPre;
+                    // accumulators kept in AGPRs until used (see below)
+#pragma unroll
+                    for (int nb = 0; nb < NB16; ++nb) asm volatile("" : "+a"(acc16[m][nb]));
+#pragma unroll
+                    for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) *(MOE_LDS u32x4*)sq(hb, 8 * i + rb, cb) = ld[k][hb][i];
+                    const uint32_t sc[2][2] = {{sl[k][0], sh[k][0]}, {sl[k][1], sh[k][1]}};
+                    asm volatile("" ::: "memory");  // a wave's LDS accesses execute in order
+                    uint32_t qa[NB16], qb[NB16];
+#pragma unroll
+                    for (int nb = 0; nb < NB16; ++nb) {
+                        qa[nb] = *(const MOE_LDS uint32_t*)(sq(0, r, nb) + 4 * q);
+                        qb[nb] = *(const MOE_LDS uint32_t*)(sq(1, r, nb) + 4 * q);
+                    }
+                    asm volatile("" ::: "memory");  // all read before the results overwrite them
+                    if (m + kPre < MB16) issue_loads(m + kPre);
+                    u32x2 hw[NB16];
+#pragma unroll
+                    for (int nb = 0; nb < NB16; ++nb) {
+                        const int sft = 8 * ((nb >> 1) & 1);  // blocks 0 and 1 of each 64 columns
+                        const float sta = step8((sc[0][nb >> 2] >> sft) & 0xffu);
+                        const float stb = step8((sc[1][nb >> 2] >> sft) & 0xffu);
+                        const float av[4] = {byte_f32<0>(qa[nb]) * sta, byte_f32<1>(qa[nb]) * sta,
+                                             byte_f32<2>(qa[nb]) * sta, byte_f32<3>(qa[nb]) * sta};
+                        const float bv[4] = {byte_f32<0>(qb[nb]) * stb, byte_f32<1>(qb[nb]) * stb,
+                                             byte_f32<2>(qb[nb]) * stb, byte_f32<3>(qb[nb]) * stb};
+                        float da[4], db[4], hv[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float v = acc16[m][nb][i], a = av[i], b = bv[i];
+                            // da = dh b s (1 + a (1 - s)), db = dh a s, h = a s b, with s = sigmoid(a)
+                            const float sg = sigmoid_f(a);
+                            const float u = v * sg, w = u * b;
+                            db[i] = u * a;
+                            da[i] = __builtin_fmaf(w, __builtin_fmaf(-a, sg, a), w);
+                            hv[i] = a * sg * b;
+                        }
+                        *(MOE_LDS u32x2*)(sa(0, r, 2 * nb + (q >> 1)) + 8 * (q & 1)) =
+                            u32x2{pack_bf2x(da[0], da[1]), pack_bf2x(da[2], da[3])};
+                        *(MOE_LDS u32x2*)(sa(1, r, 2 * nb + (q >> 1)) + 8 * (q & 1)) =
+                            u32x2{pack_bf2x(db[0], db[1]), pack_bf2x(db[2], db[3])};
+                        hw[nb] = u32x2{pack_bf2x(hv[0], hv[1]), pack_bf2x(hv[2], hv[3])};
+                    }
+                    // rows 4i + rw of the block staged in half hb to dst, at ld elements a row
+                    auto flush = [&](int hb, uint16_t* dst, int64_t ld) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const u32x4 v = *(const MOE_LDS u32x4*)sa(hb, 4 * i + rw, cc);
+                            const int mloc = row16(m) + 4 * i + rw;
+                            if (mloc < valid && n0 + 8 * cc < p.N)
+                                *(u32x4*)(dst + (int64_t)(row0 + mloc) * ld + n0 + 8 * cc) = v;
+                        }
+                    };
+                    asm volatile("" ::: "memory");
+                    flush(0, p.c, p.ldc);
+                    flush(1, p.c + p.N, p.ldc);
+                    asm volatile("" ::: "memory");  // this block's rows are read before the next is written
+                    if (p.c2) {
+#pragma unroll
+                        for (int nb = 0; nb < NB16; ++nb)
+                            *(MOE_LDS u32x2*)(sa(0, r, 2 * nb + (q >> 1)) + 8 * (q & 1)) = hw[nb];
+                        asm volatile("" ::: "memory");
+                        flush(0, p.c2, p.N);
+                        asm volatile("" ::: "memory");
+                    }
+                }
+                __syncthreads();  // every wave is done with the slot before the next stage refills it
+            } else if constexpr (EPI == EPI_SWIGLU_BWD && MOE_GEMM_DGRAD_STAGED) {  // the accumulators are dh
                 // The saved (a, b) pairs come in, and (da, db) go out, as whole
                 // 256-byte row pieces through the wave's 8 KiB of the free slot:
                 // one 16-row block at a time, a in its first 4 KiB and b in the
@@ -1044,40 +1165,18 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
                 const int ncol = ni * BN + wn * (BN / WN) + 8 * cc;  // the chunk's first column
                 const bool col_ok = ncol < p.N;
                 constexpr int kPre = MOE_GEMM_DGRAD_PREFETCH;
-                // SWIGLU_BWD8: 8 bytes and the block's scale byte per chunk of 8
-                // columns, widened to bf16 (exactly) on the way into LDS
-                typedef std::conditional_t<kBwd8, u32x2, u32x4> Saved;
-                Saved ld[kPre][2][4];
-                uint32_t ls[kBwd8 ? kPre : 1][2][4];
+                u32x4 ld[kPre][2][4];
                 auto issue_loads = [&](int m) {
-                    Saved(&l)[2][4] = ld[m % kPre];
+                    u32x4(&l)[2][4] = ld[m % kPre];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int mloc = row16(m) + 4 * i + rw;
-                        l[0][i] = l[1][i] = Saved{};
-                        if constexpr (kBwd8) ls[m % kPre][0][i] = ls[m % kPre][1][i] = 127u;
+                        l[0][i] = l[1][i] = u32x4{0u, 0u, 0u, 0u};
                         if (mloc < valid && col_ok) {
-                            const int64_t at = (int64_t)(row0 + mloc) * 2 * p.N + ncol;
-                            if constexpr (kBwd8) {
-                                l[0][i] = *(const u32x2*)(p.q8 + at);
-                                l[1][i] = *(const u32x2*)(p.q8 + at + p.N);
-                                ls[m % kPre][0][i] = p.s8[at >> 5];
-                                ls[m % kPre][1][i] = p.s8[(at + p.N) >> 5];
-                            } else {
-                                l[0][i] = *(const u32x4*)(p.ab + at);
-                                l[1][i] = *(const u32x4*)(p.ab + at + p.N);
-                            }
+                            const uint16_t* src = p.ab + (int64_t)(row0 + mloc) * 2 * p.N + ncol;
+                            l[0][i] = *(const u32x4*)src;
+                            l[1][i] = *(const u32x4*)(src + p.N);
                         }
-                    }
-                };
-                auto saved_bf16 = [&](int m, int hb, int i) {
-                    if constexpr (kBwd8) {
-                        const float step = step8(ls[m % kPre][hb][i]);
-                        const u32x2 lo = dequant8x4(ld[m % kPre][hb][i][0], step);
-                        const u32x2 hi = dequant8x4(ld[m % kPre][hb][i][1], step);
-                        return u32x4{lo[0], lo[1], hi[0], hi[1]};
-                    } else {
-                        return ld[m % kPre][hb][i];
                     }
                 };
                 // MFMA layout: row ln%16, columns 4q..4q+3 of each 16-column block
@@ -1096,16 +1195,15 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
 #pragma unroll
                     for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) *(MOE_LDS u32x4*)sa(hb, 4 * i + rw, cc) = saved_bf16(m, hb, i);
+                        for (int i = 0; i < 4; ++i) *(MOE_LDS u32x4*)sa(hb, 4 * i + rw, cc) = ld[m % kPre][hb][i];
                     asm volatile("" ::: "memory");  // a wave's LDS accesses execute in order
                     if (m + kPre < MB16) issue_loads(m + kPre);
-                    u32x2 hw[kBwd8 ? NB16 : 1];  // the block's h values, for dW_down
 #pragma unroll
                     for (int nb = 0; nb < NB16; ++nb) {
                         MOE_LDS uint8_t* pa = sa(0, r, 2 * nb + (q >> 1)) + 8 * (q & 1);
                         MOE_LDS uint8_t* pb = sa(1, r, 2 * nb + (q >> 1)) + 8 * (q & 1);
                         const u32x2 aw = *(const MOE_LDS u32x2*)pa, bw = *(const MOE_LDS u32x2*)pb;
-                        float da[4], db[4], hv[4];
+                        float da[4], db[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const float v = acc16[m][nb][i];
@@ -1116,9 +1214,7 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
                             const float u = v * sg, w = u * b;
                             db[i] = u * a;
                             da[i] = __builtin_fmaf(w, __builtin_fmaf(-a, sg, a), w);
-                            if constexpr (kBwd8) hv[i] = a * sg * b;
                         }
-                        if constexpr (kBwd8) hw[nb] = u32x2{pack_bf2x(hv[0], hv[1]), pack_bf2x(hv[2], hv[3])};
                         *(MOE_LDS u32x2*)pa = u32x2{pack_bf2x(da[0], da[1]), pack_bf2x(da[2], da[3])};
                         *(MOE_LDS u32x2*)pb = u32x2{pack_bf2x(db[0], db[1]), pack_bf2x(db[2], db[3])};
                     }
@@ -1133,23 +1229,6 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
                                 *(u32x4*)(p.c + (int64_t)(row0 + mloc) * p.ldc + hb * p.N + ncol) = v;
                         }
                     asm volatile("" ::: "memory");  // this block's rows are read before the next is written
-                    if constexpr (kBwd8) {
-                        if (p.c2) {
-                            // h takes the same way out
-#pragma unroll
-                            for (int nb = 0; nb < NB16; ++nb)
-                                *(MOE_LDS u32x2*)(sa(0, r, 2 * nb + (q >> 1)) + 8 * (q & 1)) = hw[nb];
-                            asm volatile("" ::: "memory");
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const u32x4 v = *(const MOE_LDS u32x4*)sa(0, 4 * i + rw, cc);
-                                const int mloc = row16(m) + 4 * i + rw;
-                                if (mloc < valid && col_ok)
-                                    *(u32x4*)(p.c2 + (int64_t)(row0 + mloc) * p.N + ncol) = v;
-                            }
-                            asm volatile("" ::: "memory");
-                        }
-                    }
                 }
                 __syncthreads();  // every wave is done with the slot before the next stage refills it
             } else if constexpr (EPI == EPI_SWIGLU_BWD) {  // the accumulators are dh
@@ -1391,7 +1470,7 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
             __syncthreads();  // every wave is done with the slot before the next stage refills it
             continue;
         }
-        if constexpr (EPI == EPI_SWIGLU && NTW == 4 && !GATHER) {
+        if constexpr (((EPI == EPI_SWIGLU && !GATHER) || EPI == EPI_SWIGLU8) && NTW == 4) {
             // SwiGLU outputs go out through LDS as the bf16 ones do: each wave
             // holds 64 columns of h (and of a and b) per 32-row block, one 4 KiB
             // staging block of 32 rows x 128 bytes, stored as whole lines.  Stored
@@ -1416,6 +1495,24 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
                     const int mloc = row_base(mt) + rr;
                     const int n = hc0 + 8 * c;
                     if (mloc < valid && n < p.N) *(u32x4*)(dst + (int64_t)(row0 + mloc) * ld + col0 + n) = v;
+                }
+            };
+            // the staged a or b rows (32 bf16 of a block in 4 lanes) as 8-bit blocks: 64
+            // bytes of a row per 8 lanes, and its two scale bytes
+            auto flush8 = [&](int buf, int mt, int half) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int rr = 8 * i + (ln >> 3), c = ln & 7;
+                    const u32x4 v = *(const MOE_LDS u32x4*)stage_addr(buf, rr, c);
+                    uint32_t s;
+                    const u32x2 q = pack8_lane(v, s);
+                    const int mloc = row_base(mt) + rr;
+                    const int n = hc0 + 8 * c;
+                    if (mloc < valid && n < p.N) {
+                        const int64_t at = (int64_t)(row0 + mloc) * 2 * p.N + half * p.N + n;
+                        *(u32x2*)(p.q8 + at) = q;
+                        if ((c & 3) == 0) p.s8[at >> 5] = (uint8_t)s;
+                    }
                 }
             };
             // lane (r, hh) holds columns 8*j4 + 4*hh + 0..3 of 32-column block i2 in row r
@@ -1448,7 +1545,19 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
                         put(0, i2, j4, u32x2{pack_bf2x(hv[0], hv[1]), pack_bf2x(hv[2], hv[3])});
                     }
                 }
-                if (p.c2) {
+                if constexpr (EPI == EPI_SWIGLU8) {
+                    if (kBufs == 2) {
+                        put_ab(kBufs - 1, mt, 0);
+                        flush(0, mt, p.c, p.ldc, 0);
+                        flush8(kBufs - 1, mt, 0);
+                    } else {
+                        flush(0, mt, p.c, p.ldc, 0);
+                        put_ab(0, mt, 0);
+                        flush8(0, mt, 0);
+                    }
+                    put_ab(0, mt, 1);
+                    flush8(0, mt, 1);
+                } else if (p.c2) {
                     if (kBufs == 2) {
                         // h and a staged together, then b
                         put_ab(kBufs - 1, mt, 0);
@@ -1522,7 +1631,8 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
                             m = max_mag2(m, w[i] & 0x7fff7fffu);
                         }
                         m = max(m & 0xffffu, m >> 16);
-                        m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+                        const auto sw = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+                        m = max((uint32_t)sw[0], (uint32_t)sw[1]);  // with lane ^ 32
                         const uint32_t sc = scale8_of(m);
                         const float inv = inv_step8(sc);
                         uint32_t d[4];
@@ -1833,6 +1943,16 @@ static int launch(const GemmParams& p, hipStream_t s) {
             return launch_cfg<256, 256, 32, 2, 2, LB, EPI, SCHED, kLdsBudget, 192, GATHER>(p, s);
     }
     return launch_cfg<256, 256, 32, 2, 2, LB, EPI, SCHED, kLdsBudget, 0, GATHER>(p, s);
+}
+
+// The 8-bit forms' small grids: whether tiles of bm rows x cols columns all fit
+// the chip at once, two per CU, going by the sizes (an expert has cap / e_local
+// rows on average).  Larger tiles would then leave most CUs idle, and a tile's
+// epilogue, one wave per SIMD, is as long as the tile is large.
+inline bool fits_chip(const GemmParams& p, int bm, int cols) {
+    if (tile_config() != CFG_AUTO) return false;
+    const int64_t avg = (p.cap + p.e_local - 1) / p.e_local;
+    return (avg + bm - 1) / bm * p.e_local * ((p.N + cols - 1) / cols) <= 2 * (int64_t)moe_host::num_cus();
 }
 
 // Launchers of the instantiations, each compiled in one translation unit

@@ -4,6 +4,21 @@
 
 using moe_host::misaligned;
 
+namespace moe {
+
+// Tiles of 64 rows x 64 columns of h while the chip holds them all: 8 experts of
+// 64 rows, H = 128, F = 256 (32 tiles) 7.4 us against 14.3 with the large ones; 32 of
+// 64, H = 1024, F = 512 (256) 24 against 32; 32 of 34, H = 7168, F = 2048 (1024) 350
+// against 296.
+template <bool GATHER>
+static int launch_save8(const GemmParams& p, hipStream_t s) {
+    if (fits_chip(p, 64, 64))
+        return launch_cfg<64, 128, 32, 2, 2, LAY_MN, EPI_SWIGLU8, SCHED_ROWS, kLdsBudget, 0, GATHER>(p, s);
+    return launch<LAY_MN, EPI_SWIGLU8, SCHED_ROWS, GATHER>(p, s);
+}
+
+}  // namespace moe
+
 extern "C" int moe_grouped_gemm_swiglu_save8(const moe_bf16* x_perm, const moe_bf16* w_gate, const moe_bf16* w_up,
                                              const int32_t* offsets, int e_local, int H, int F, int cap_rows,
                                              moe_bf16* h, int8_t* ab8, uint8_t* ab8_scale, moe_stream stream) {
@@ -34,7 +49,7 @@ extern "C" int moe_grouped_gemm_swiglu_save8(const moe_bf16* x_perm, const moe_b
     p.ldc = F;
     p.q8 = ab8;
     p.s8 = ab8_scale;
-    return launch<LAY_MN, EPI_SWIGLU8, SCHED_ROWS>(p, (hipStream_t)stream);
+    return launch_save8<false>(p, (hipStream_t)stream);
 }
 
 extern "C" int moe_grouped_gemm_swiglu_gather_save8(const moe_bf16* x, int T, const int32_t* src, int K,
@@ -75,5 +90,5 @@ extern "C" int moe_grouped_gemm_swiglu_gather_save8(const moe_bf16* x, int T, co
     p.ldc = F;
     p.q8 = ab8;
     p.s8 = ab8_scale;
-    return launch<LAY_MN, EPI_SWIGLU8, SCHED_ROWS, true>(p, (hipStream_t)stream);
+    return launch_save8<true>(p, (hipStream_t)stream);
 }

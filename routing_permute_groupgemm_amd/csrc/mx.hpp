@@ -56,6 +56,22 @@ __device__ __forceinline__ uint32_t quant8x4(float x0, float x1, float x2, float
     return lo | hi;
 }
 
+// 8 bf16 of a block that four neighbouring lanes hold (lanes 4i .. 4i+3) to
+// their bytes; s is the block's scale byte, the same in the four lanes.
+__device__ __forceinline__ u32x2 pack8_lane(u32x4 v, uint32_t& s) {
+    uint32_t m = max_mag2(max_mag2(v[0] & 0x7fff7fffu, v[1] & 0x7fff7fffu),
+                          max_mag2(v[2] & 0x7fff7fffu, v[3] & 0x7fff7fffu));
+    m = max(m & 0xffffu, m >> 16);
+    m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xb1, 0xf, 0xf, true));  // lane ^ 1
+    m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4e, 0xf, 0xf, true));  // lane ^ 2
+    s = scale8_of(m);
+    const float inv = inv_step8(s);
+    u32x2 o = {quant8x4(bf_lo(v[0]), bf_hi(v[0]), bf_lo(v[1]), bf_hi(v[1]), inv),
+               quant8x4(bf_lo(v[2]), bf_hi(v[2]), bf_lo(v[3]), bf_hi(v[3]), inv)};
+    if (s == 255u) o = u32x2{0u, 0u};
+    return o;
+}
+
 // Signed byte i of w as a float.
 template <int I>
 __device__ __forceinline__ float byte_f32(uint32_t w) {
