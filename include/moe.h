@@ -479,7 +479,8 @@ int moe_grouped_gemm4(const moe_bf16* a, const uint8_t* q4, const uint8_t* s4, c
  * moe_grouped_gemm4 and moe_combine in one, without rounding the experts' rows
  * to bf16 in between:
  *   out[t] = bf16(sum over k ascending with 0 <= pos[t,k] < cap_rows of gates[t,k] * (a[pos[t,k]] . w))
- * A token without such a pair gets +0.  y, if not NULL, is moe_grouped_gemm4's c.
+ * A token without such a pair gets +0.  y, if not NULL, gets the rows a[r] . w rounded
+ * to bf16.
  *   pos int32 [T,K], gates fp32 [T,K];  y bf16 [cap_rows,N] or NULL;  out bf16 [T,N];
  *   ws: device workspace of at least moe_gemm4_combine_workspace_size(cap_rows, N)
  *   bytes (the fp32 rows).  T <= 262140; MOE_EWORKSPACE if ws is NULL or too small.

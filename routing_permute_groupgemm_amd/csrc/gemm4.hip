@@ -150,6 +150,15 @@ __device__ __forceinline__ void column_tiles(const Gemm4Params& p, int j, int nt
     for (int i = 0; i < NT; ++i) at[i] = ((int64_t)j * n + min(nt0 + i, n - 1)) * p.KT;
 }
 
+// Eight codes times their block's scale, as bf16.
+__device__ __forceinline__ bf16x8 fp4_step(uint32_t d, float f) {
+    const u32x4 v = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, f, 0)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, f, 1)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, f, 2)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, f, 3))};
+    return __builtin_bit_cast(bf16x8, v);
+}
+
 // One contraction tile of a wave's weights: NT column tiles of each matrix.
 template <int MATS, int NT>
 struct Weights4 {
@@ -169,13 +178,7 @@ struct Weights4 {
     }
     // Step st (8 of each lane's 32 contraction values) as bf16.
     __device__ __forceinline__ bf16x8 step(int q, int i, int st) const {
-        const float f = __uint_as_float(s[q][i] << 23);
-        const uint32_t d = w[q][i][st];
-        const u32x4 v = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, f, 0)),
-                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, f, 1)),
-                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, f, 2)),
-                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, f, 3))};
-        return __builtin_bit_cast(bf16x8, v);
+        return fp4_step(w[q][i][st], __uint_as_float(s[q][i] << 23));
     }
 };
 
@@ -275,17 +278,20 @@ __global__ __launch_bounds__(64 * W) void gemm4_split(Gemm4Params p) {
     }
 }
 
-// 16*MT rows x 64*NT columns of a workgroup of four waves.  A contraction tile of
+// 16*MT rows x 16*NT*W columns of a workgroup of W waves.  A contraction tile of
 // the rows is [16*MT][128] bf16 in LDS, 256-byte rows with their 16-byte chunks
 // XOR-swizzled by row; two such buffers and one barrier a tile (a wave that
 // writes buffer b for tile k+2 has passed the barrier of tile k+1, which every
 // wave reaches after its reads of tile k).  Rows and weights of the next
 // tile are in flight while one is multiplied; deeper prefetch of the weights
-// (3 and 4 tiles) cost registers, and with them waves, and ran slower.
+// (3 and 4 tiles) cost registers, and with them waves, and ran slower.  Row blocks
+// past the tile's rows are neither read nor multiplied.
 // NTL: the weights carry the non-temporal hint (see launch4_rows).
-template <int MATS, int MT, int NT, bool NTL>
-__global__ __launch_bounds__(256) void gemm4_wide(Gemm4Params p) {
-    constexpr int W = 4;
+template <int MATS, int MT, int NT, int W, bool NTL>
+__global__ __launch_bounds__(64 * W) void gemm4_wide(Gemm4Params p) {
+    // a thread's 16-byte loads of the rows per tile, and the rows that one of them covers
+    constexpr int XL = MT * 4 / W, XR = 4 * W;
+    static_assert(XL * W == MT * 4, "the rows' loads split evenly over the threads");
     __shared__ __attribute__((aligned(16))) uint8_t xs[2][MT * 4096];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -300,25 +306,25 @@ __global__ __launch_bounds__(256) void gemm4_wide(Gemm4Params p) {
     Weights4<MATS, NT> wb[2];
     wb[0].template load<NTL>(p, tiles, 0, lane);  // does not wait for the rows' indices
     const auto rs = rows_rsrc(p, row0, rows);
-    const int xrow = tid >> 4, xch = tid & 15;  // this thread's 16-byte chunk of rows xrow + 16*m
-    uint32_t off[MT];
+    const int xrow = tid >> 4, xch = tid & 15;  // this thread's 16-byte chunk of rows xrow + XR*m
+    uint32_t off[XL];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        off[m] = row_offset(p, row0, rows, 16 * m + xrow);
+    for (int m = 0; m < XL; ++m) {
+        off[m] = row_offset(p, row0, rows, XR * m + xrow);
         if (off[m] != kNoRow) off[m] += 16u * xch;
     }
-    u32x4 xr[2][MT];
-    auto load_x = [&](u32x4 (&x)[MT], int kt) {
+    u32x4 xr[2][XL];
+    auto load_x = [&](u32x4 (&x)[XL], int kt) {
         const bool in = kt * 128 + 8 * xch < p.Kd;  // 0 behind the contraction's end
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < XL; ++m)
             x[m] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
                                                  rs, (in ? off[m] : kNoRow) + (uint32_t)(kt * 256), 0, 0));
     };
-    auto put_x = [&](const u32x4 (&x)[MT], int slot) {
+    auto put_x = [&](const u32x4 (&x)[XL], int slot) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-            *(MOE_LDS u32x4*)(xs[slot] + (16 * m + xrow) * 256 + ((xch ^ xrow) << 4)) = x[m];
+        for (int m = 0; m < XL; ++m)
+            *(MOE_LDS u32x4*)(xs[slot] + (XR * m + xrow) * 256 + ((xch ^ (xrow & 15)) << 4)) = x[m];
     };
     f32x4 acc[MATS][NT][MT];
 #pragma unroll
@@ -333,8 +339,9 @@ __global__ __launch_bounds__(256) void gemm4_wide(Gemm4Params p) {
             bf16x8 xf[MT];
 #pragma unroll
             for (int m = 0; m < MT; ++m)
-                xf[m] = __builtin_bit_cast(
-                    bf16x8, *(const MOE_LDS u32x4*)(xs[slot] + (16 * m + r16) * 256 + (((4 * g + st) ^ r16) << 4)));
+                if (m == 0 || 16 * m < rows)
+                    xf[m] = __builtin_bit_cast(bf16x8, *(const MOE_LDS u32x4*)(xs[slot] + (16 * m + r16) * 256 +
+                                                                               (((4 * g + st) ^ r16) << 4)));
 #pragma unroll
             for (int q = 0; q < MATS; ++q)
 #pragma unroll
@@ -342,7 +349,8 @@ __global__ __launch_bounds__(256) void gemm4_wide(Gemm4Params p) {
                     const bf16x8 wv = w.step(q, i, st);
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
-                        acc[q][i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, xf[m], acc[q][i][m], 0, 0, 0);
+                        if (m == 0 || 16 * m < rows)
+                            acc[q][i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, xf[m], acc[q][i][m], 0, 0, 0);
                 }
         }
     };
@@ -380,12 +388,12 @@ static int launch_split(const Gemm4Params& p, hipStream_t s) {
     return moe_host::launch_status();
 }
 
-template <int MATS, int MT, int NT, bool NTL>
+template <int MATS, int MT, int NT, int W, bool NTL>
 static int launch_wide(const Gemm4Params& p, hipStream_t s) {
     const int64_t tiles = std::min<int64_t>(p.cap, p.cap / (16 * MT) + p.e_local);
-    const int64_t grid = (tiles * ((p.N / 16 + NT * 4 - 1) / (NT * 4)) + 7) / 8 * 8;
+    const int64_t grid = (tiles * ((p.N / 16 + NT * W - 1) / (NT * W)) + 7) / 8 * 8;
     if (grid >= (1ll << 31)) return MOE_EINVAL;
-    gemm4_wide<MATS, MT, NT, NTL><<<(unsigned)grid, 256, 0, s>>>(p);
+    gemm4_wide<MATS, MT, NT, W, NTL><<<(unsigned)grid, 64 * W, 0, s>>>(p);
     return moe_host::launch_status();
 }
 
@@ -398,8 +406,7 @@ static int launch_wide(const Gemm4Params& p, hipStream_t s) {
 //     make 512 workgroups, two a CU (gate/up of two tokens 19.9 against 22.9 us, of
 //     one 12.8 against 11.7).
 //   wide: row tiles of 16, or of 32 when there are more than 16 rows an expert
-//     (gate/up of 512 tokens, 128 experts: 183 against 207 us; 64 rows were slower
-//     at every size, the accumulators leaving too few waves).
+//     (gate/up of 512 tokens, 128 experts: 183 against 207 us; 64 rows took 186 to 220).
 //   non-temporal weights: when the packed matrices that the rows can touch
 //     fill half the last-level cache (128 MB) or more, so that they are not there the
 //     next time, and an expert's rows mostly fit one tile (three quarters of it or
@@ -417,16 +424,16 @@ static int launch4_rows(const Gemm4Params& p, hipStream_t s) {
     const int64_t experts = std::min<int64_t>(p.cap, p.e_local);
     const bool large = experts * MATS * p.N * p.Kd * 17 / 32 >= (128ll << 20);
     if (p.cap <= 16ll * p.e_local) {
-        if (large && p.cap <= 12ll * p.e_local) return launch_wide<MATS, 1, 2 / MATS, true>(p, s);
-        return launch_wide<MATS, 1, 2 / MATS, false>(p, s);
+        if (large && p.cap <= 12ll * p.e_local) return launch_wide<MATS, 1, 2 / MATS, 4, true>(p, s);
+        return launch_wide<MATS, 1, 2 / MATS, 4, false>(p, s);
     }
     if (p.cap <= 24ll * p.e_local) {
-        if (large) return launch_wide<MATS, 2, 2, true>(p, s);
-        return launch_wide<MATS, 2, 2, false>(p, s);
+        if (large) return launch_wide<MATS, 2, 1, 8, true>(p, s);
+        return launch_wide<MATS, 2, 1, 8, false>(p, s);
     }
-    // several row tiles an expert: down takes 256 columns a workgroup, reading the rows half as often
-    // (512 tokens: 110 against 125 us; gate/up has no registers left for it)
-    return launch_wide<MATS, 2, 4 / MATS, false>(p, s);
+    // several row tiles an expert: 256 columns a workgroup, so that the rows are read half as often (512
+    // tokens: gate/up 179 against 183 us, down 108 against 126; 2048 tokens: 428 against 462 and 269 against 342)
+    return launch_wide<MATS, 2, 2, 8, false>(p, s);
 }
 
 // out[t] = bf16(sum over k ascending of gate[t,k] * y[pos[t,k]]) from fp32 rows: moe_combine without the rounding
