@@ -103,15 +103,29 @@ def _stream(stream):
     return stream.cuda_stream
 
 
-def _on_device(stream, *tensors):
-    """The stream's handle, after checking that it and every tensor are on the current device."""
+def _device(stream, t):
+    """The current device, which the stream (None: its current one) must belong to; t: a first argument, refused
+    here if it is on the host (there may be no device then)."""
+    if not t.is_cuda:
+        raise MoeError(f"expected CUDA tensors, got one on {t.device}")
     dev = torch.cuda.current_device()
     if stream is not None and stream.device_index != dev:
         raise MoeError(f"a stream of device {stream.device_index} with device {dev} current")
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise MoeError(f"a tensor on {t.device} with device {dev} current")
-    return _stream(stream)
+    return dev
+
+
+def _arg(t, dtype, name, dev):
+    """A contiguous tensor of this type on this device."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise MoeError(f"{name}: expected a contiguous {dtype} tensor on CUDA device {dev}, got {t.dtype} "
+                       f"contiguous={t.is_contiguous()} device={t.device}")
+
+
+def _handle(stream, dev):
+    """The stream's handle, dev being the current device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
 def _need(t, dtype, name):
@@ -122,7 +136,7 @@ def _need(t, dtype, name):
 
 def _shape(t, shape, name):
     """A caller-provided buffer must have exactly this shape (the kernels write all of it)."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise MoeError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -542,130 +556,126 @@ def moe_router_backward(x, w_r, dlogits, dx=None, dw_r=None, ws=None, stream=Non
     return dx, dw_r
 
 
-def _routed(offsets):
+def _routed(offsets, dev):
     """offsets or None -> its expert count (0 without)."""
     if offsets is None:
         return 0
-    _need(offsets, torch.int32, "offsets")
+    _arg(offsets, torch.int32, "offsets", dev)
     if offsets.dim() != 1 or offsets.numel() < 1:
         raise MoeError(f"offsets: expected e_local + 1 entries, got {tuple(offsets.shape)}")
     return offsets.numel() - 1
 
 
-def _save8(q, scale, rows, cols, dev, names=("q", "scale")):
-    """The caller's 8-bit buffers (checked: at least `rows` rows) or new ones."""
-    if q is None:
-        q = torch.empty((rows, cols), dtype=torch.int8, device=dev)
-    if scale is None:
-        scale = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
-    _need(q, torch.int8, names[0])
-    _need(scale, torch.uint8, names[1])
-    _rows(q, rows, cols, names[0])
-    _rows(scale, rows, cols // 32, names[1])
-    return q, scale
+def _offsets(offsets, EL, dev):
+    _arg(offsets, torch.int32, "offsets", dev)
+    if offsets.numel() < EL + 1:
+        raise MoeError(f"offsets: expected {EL + 1} entries, got {offsets.numel()}")
+
+
+def _out(t, shape, dtype, name, dev, rows=None):
+    """The caller's buffer (checked: at least `rows` rows, or exactly `shape`) or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
+    _arg(t, dtype, name, dev)
+    if rows is None:
+        _shape(t, shape, name)
+    else:
+        _rows(t, rows, shape[1], name)
+    return t
 
 
 def moe_pack8(x, q=None, scale=None, offsets=None, stream=None):
     """Rows of bf16 -> (q int8 [rows, cols], scale uint8 [rows, cols/32]) in blocks of 32 columns.
     offsets (int32 [e_local+1]): only the first offsets[e_local] rows are read and written."""
-    _need(x, torch.bfloat16, "x")
-    if x.dim() != 2:
-        raise MoeError(f"x: expected [rows, cols], got {tuple(x.shape)}")
+    dev = _device(stream, x)
+    _arg(x, torch.bfloat16, "x", dev)
+    if x.dim() != 2 or x.shape[1] % 64:
+        raise MoeError(f"x: expected [rows, a multiple of 64], got {tuple(x.shape)}")
     rows, cols = x.shape
-    q, scale = _save8(q, scale, rows, cols, x.device)
-    _check(load().moe_pack8(_ptr(x), rows, cols, _ptr(offsets), _routed(offsets), _ptr(q), _ptr(scale),
-                            _on_device(stream, x, offsets, q, scale)))
+    EL = _routed(offsets, dev)
+    q = _out(q, (rows, cols), torch.int8, "q", dev, rows)
+    scale = _out(scale, (rows, cols // 32), torch.uint8, "scale", dev, rows)
+    _check(load().moe_pack8(_ptr(x), rows, cols, _ptr(offsets), EL, _ptr(q), _ptr(scale), _handle(stream, dev)))
     return q, scale
 
 
 def moe_unpack8(q, scale, x=None, offsets=None, stream=None):
     """The bf16 rows that (q, scale) stand for (rows and offsets as moe_pack8)."""
-    _need(q, torch.int8, "q")
-    _need(scale, torch.uint8, "scale")
-    if q.dim() != 2:
-        raise MoeError(f"q: expected [rows, cols], got {tuple(q.shape)}")
+    dev = _device(stream, q)
+    _arg(q, torch.int8, "q", dev)
+    _arg(scale, torch.uint8, "scale", dev)
+    if q.dim() != 2 or q.shape[1] % 64:
+        raise MoeError(f"q: expected [rows, a multiple of 64], got {tuple(q.shape)}")
     rows, cols = q.shape
+    EL = _routed(offsets, dev)
     _rows(scale, rows, cols // 32, "scale")
-    if x is None:
-        x = torch.empty((rows, cols), dtype=torch.bfloat16, device=q.device)
-    _need(x, torch.bfloat16, "x")
-    _rows(x, rows, cols, "x")
-    _check(load().moe_unpack8(_ptr(q), _ptr(scale), rows, cols, _ptr(offsets), _routed(offsets), _ptr(x),
-                              _on_device(stream, q, scale, offsets, x)))
+    x = _out(x, (rows, cols), torch.bfloat16, "x", dev, rows)
+    _check(load().moe_unpack8(_ptr(q), _ptr(scale), rows, cols, _ptr(offsets), EL, _ptr(x), _handle(stream, dev)))
     return x
+
+
+def _save8_args(x, w_gate, w_up, offsets, cap_rows, h, ab8, ab8_scale, dev):
+    """Checks common to the two forms -> (EL, H, F, h, ab8, ab8_scale)."""
+    for t, name in ((x, "x"), (w_gate, "w_gate"), (w_up, "w_up")):
+        _arg(t, torch.bfloat16, name, dev)
+    if w_gate.dim() != 3:
+        raise MoeError(f"w_gate: expected [E, H, F], got {tuple(w_gate.shape)}")
+    EL, H, F = w_gate.shape
+    _shape(w_up, (EL, H, F), "w_up")
+    _offsets(offsets, EL, dev)
+    n = max(cap_rows, 0)
+    h = _out(h, (n, F), torch.bfloat16, "h", dev, n)
+    ab8 = _out(ab8, (n, 2 * F), torch.int8, "ab8", dev, n)
+    ab8_scale = _out(ab8_scale, (n, 2 * F // 32), torch.uint8, "ab8_scale", dev, n)
+    return EL, H, F, h, ab8, ab8_scale
 
 
 def moe_grouped_gemm_swiglu_save8(x_perm, w_gate, w_up, offsets, cap_rows, h=None, ab8=None, ab8_scale=None,
                                   stream=None):
     """moe_grouped_gemm_swiglu with (a, b) saved in 8-bit blocks -> (h, ab8, ab8_scale)."""
-    _need(x_perm, torch.bfloat16, "x_perm")
-    _need(w_gate, torch.bfloat16, "w_gate")
-    _need(w_up, torch.bfloat16, "w_up")
-    _need(offsets, torch.int32, "offsets")
-    EL, H, F = w_gate.shape
-    if h is None:
-        h = torch.empty((max(cap_rows, 1), F), dtype=torch.bfloat16, device=x_perm.device)
-    _gate_up_checks(w_gate, w_up, offsets, cap_rows, h, None)
-    ab8, ab8_scale = _save8(ab8, ab8_scale, max(cap_rows, 0), 2 * F, x_perm.device, ("ab8", "ab8_scale"))
+    dev = _device(stream, x_perm)
+    EL, H, F, h, ab8, ab8_scale = _save8_args(x_perm, w_gate, w_up, offsets, cap_rows, h, ab8, ab8_scale, dev)
     _rows(x_perm, cap_rows, H, "x_perm")
     _check(load().moe_grouped_gemm_swiglu_save8(_ptr(x_perm), _ptr(w_gate), _ptr(w_up), _ptr(offsets), EL, H, F,
-                                                cap_rows, _ptr(h), _ptr(ab8), _ptr(ab8_scale),
-                                                _on_device(stream, x_perm, w_gate, w_up, offsets, h, ab8, ab8_scale)))
+                                                cap_rows, _ptr(h), _ptr(ab8), _ptr(ab8_scale), _handle(stream, dev)))
     return h, ab8, ab8_scale
 
 
 def moe_grouped_gemm_swiglu_gather_save8(x, src, K, w_gate, w_up, offsets, cap_rows, h=None, ab8=None,
                                          ab8_scale=None, stream=None):
     """The same, reading row r of the expert-grouped order from x[src[r] // K] (no x_perm)."""
-    _need(x, torch.bfloat16, "x")
-    _need(src, torch.int32, "src")
-    _need(w_gate, torch.bfloat16, "w_gate")
-    _need(w_up, torch.bfloat16, "w_up")
-    _need(offsets, torch.int32, "offsets")
-    EL, H, F = w_gate.shape
-    T = x.shape[0]
-    if h is None:
-        h = torch.empty((max(cap_rows, 1), F), dtype=torch.bfloat16, device=x.device)
-    _gate_up_checks(w_gate, w_up, offsets, cap_rows, h, None)
-    ab8, ab8_scale = _save8(ab8, ab8_scale, max(cap_rows, 0), 2 * F, x.device, ("ab8", "ab8_scale"))
-    _shape(x, (T, H), "x")
+    dev = _device(stream, x)
+    EL, H, F, h, ab8, ab8_scale = _save8_args(x, w_gate, w_up, offsets, cap_rows, h, ab8, ab8_scale, dev)
+    _rows(x, 0, H, "x")
+    _arg(src, torch.int32, "src", dev)
     if src.numel() < cap_rows:
         raise MoeError(f"src: expected at least {cap_rows} entries, got {src.numel()}")
-    _check(load().moe_grouped_gemm_swiglu_gather_save8(_ptr(x), T, _ptr(src), int(K), _ptr(w_gate), _ptr(w_up),
-                                                       _ptr(offsets), EL, H, F, cap_rows, _ptr(h), _ptr(ab8),
-                                                       _ptr(ab8_scale),
-                                                       _on_device(stream, x, src, w_gate, w_up, offsets, h, ab8,
-                                                                  ab8_scale)))
+    _check(load().moe_grouped_gemm_swiglu_gather_save8(_ptr(x), x.shape[0], _ptr(src), int(K), _ptr(w_gate),
+                                                       _ptr(w_up), _ptr(offsets), EL, H, F, cap_rows, _ptr(h),
+                                                       _ptr(ab8), _ptr(ab8_scale), _handle(stream, dev)))
     return h, ab8, ab8_scale
 
 
 def moe_grouped_gemm_swiglu_bwd8(dy_perm, w_down, offsets, cap_rows, ab8, ab8_scale, dab=None, h=None,
                                  want_h=True, stream=None):
     """Down dgrad and SwiGLU backward from the 8-bit (a, b) -> (dab, h); want_h=False: h is not recomputed."""
-    _need(dy_perm, torch.bfloat16, "dy_perm")
-    _need(w_down, torch.bfloat16, "w_down")
-    _need(offsets, torch.int32, "offsets")
+    dev = _device(stream, dy_perm)
+    _arg(dy_perm, torch.bfloat16, "dy_perm", dev)
+    _arg(w_down, torch.bfloat16, "w_down", dev)
+    if w_down.dim() != 3:
+        raise MoeError(f"w_down: expected [E, F, H], got {tuple(w_down.shape)}")
     EL, F, H = w_down.shape
-    if offsets.numel() < EL + 1:
-        raise MoeError(f"offsets: expected {EL + 1} entries, got {offsets.numel()}")
+    _offsets(offsets, EL, dev)
     _rows(dy_perm, cap_rows, H, "dy_perm")
-    for t, dt, cols, name in ((ab8, torch.int8, 2 * F, "ab8"), (ab8_scale, torch.uint8, 2 * F // 32, "ab8_scale")):
-        _need(t, dt, name)
-        _rows(t, cap_rows, cols, name)
-    if dab is None:
-        dab = torch.empty((max(cap_rows, 1), 2 * F), dtype=torch.bfloat16, device=dy_perm.device)
-    if h is None and want_h:
-        h = torch.empty((max(cap_rows, 1), F), dtype=torch.bfloat16, device=dy_perm.device)
-    if not want_h:
-        h = None
-    _need(dab, torch.bfloat16, "dab")
-    _rows(dab, cap_rows, 2 * F, "dab")
-    if h is not None:
-        _need(h, torch.bfloat16, "h")
-        _rows(h, cap_rows, F, "h")
+    _arg(ab8, torch.int8, "ab8", dev)
+    _rows(ab8, cap_rows, 2 * F, "ab8")
+    _arg(ab8_scale, torch.uint8, "ab8_scale", dev)
+    _rows(ab8_scale, cap_rows, 2 * F // 32, "ab8_scale")
+    n = max(cap_rows, 0)
+    dab = _out(dab, (n, 2 * F), torch.bfloat16, "dab", dev, n)
+    h = _out(h, (n, F), torch.bfloat16, "h", dev, n) if want_h else None
     _check(load().moe_grouped_gemm_swiglu_bwd8(_ptr(dy_perm), _ptr(w_down), _ptr(offsets), EL, H, F, cap_rows,
-                                               _ptr(ab8), _ptr(ab8_scale), _ptr(dab), _ptr(h),
-                                               _on_device(stream, dy_perm, w_down, offsets, ab8, ab8_scale, dab, h)))
+                                               _ptr(ab8), _ptr(ab8_scale), _ptr(dab), _ptr(h), _handle(stream, dev)))
     return dab, h
 
 
@@ -675,94 +685,82 @@ def pack4_shapes(E, Kd, N):
     return (E, N // 16, KT, 64, 16), (E, N // 16, KT, 64)
 
 
-def _weights4(w, Kd, name, E=None, N=None):
+def _weights4(w, Kd, name, dev, E=None, N=None):
     """Checks a (q4, s4) pair against the contraction length -> (q4, s4, E, N)."""
     q4, s4 = w
-    _need(q4, torch.uint8, name + " q4")
-    _need(s4, torch.uint8, name + " s4")
-    if q4.dim() != 5:
-        raise MoeError(f"{name} q4: expected {len(pack4_shapes(1, 64, 64)[0])} dimensions, got {tuple(q4.shape)}")
-    E = q4.shape[0] if E is None else E
-    N = q4.shape[1] * 16 if N is None else N
-    shapes = pack4_shapes(E, Kd, N)
-    _shape(q4, shapes[0], name + " q4")
-    _shape(s4, shapes[1], name + " s4")
+    _arg(q4, torch.uint8, name, dev)
+    _arg(s4, torch.uint8, name, dev)
+    if E is None:
+        if q4.dim() != 5:
+            raise MoeError(f"{name}: expected 5 dimensions of q4, got {tuple(q4.shape)}")
+        E, N = q4.shape[0], q4.shape[1] * 16
+    q_shape, s_shape = pack4_shapes(E, Kd, N)
+    _shape(q4, q_shape, name)
+    _shape(s4, s_shape, name)
     return q4, s4, E, N
 
 
 def moe_pack4(w, q4=None, s4=None, stream=None):
     """Weights bf16 [E, Kd, N] -> (q4, s4) in 4-bit blocks of 32 along Kd (layout in moe.h)."""
-    _need(w, torch.bfloat16, "w")
-    if w.dim() != 3:
-        raise MoeError(f"w: expected [E, Kd, N], got {tuple(w.shape)}")
+    dev = _device(stream, w)
+    _arg(w, torch.bfloat16, "w", dev)
+    if w.dim() != 3 or w.shape[1] % 64 or w.shape[2] % 64:
+        raise MoeError(f"w: expected [E, Kd, N] with Kd and N multiples of 64, got {tuple(w.shape)}")
     E, Kd, N = w.shape
-    if Kd % 64 or N % 64:
-        raise MoeError(f"w: Kd and N must be multiples of 64, got {tuple(w.shape)}")
-    shapes = pack4_shapes(E, Kd, N)
-    if q4 is None:
-        q4 = torch.empty(shapes[0], dtype=torch.uint8, device=w.device)
-    if s4 is None:
-        s4 = torch.empty(shapes[1], dtype=torch.uint8, device=w.device)
-    _weights4((q4, s4), Kd, "w", E, N)
-    _check(load().moe_pack4(_ptr(w), E, Kd, N, _ptr(q4), _ptr(s4), _on_device(stream, w, q4, s4)))
+    q_shape, s_shape = pack4_shapes(E, Kd, N)
+    q4 = _out(q4, q_shape, torch.uint8, "q4", dev)
+    s4 = _out(s4, s_shape, torch.uint8, "s4", dev)
+    _check(load().moe_pack4(_ptr(w), E, Kd, N, _ptr(q4), _ptr(s4), _handle(stream, dev)))
     return q4, s4
 
 
 def moe_unpack4(q4, s4, Kd, w=None, stream=None):
     """The bf16 weights [E, Kd, N] that (q4, s4) stand for."""
-    q4, s4, E, N = _weights4((q4, s4), Kd, "w")
-    if w is None:
-        w = torch.empty((E, Kd, N), dtype=torch.bfloat16, device=q4.device)
-    _need(w, torch.bfloat16, "w")
-    _shape(w, (E, Kd, N), "w")
-    _check(load().moe_unpack4(_ptr(q4), _ptr(s4), E, Kd, N, _ptr(w), _on_device(stream, q4, s4, w)))
+    dev = _device(stream, q4)
+    q4, s4, E, N = _weights4((q4, s4), Kd, "w", dev)
+    w = _out(w, (E, Kd, N), torch.bfloat16, "w", dev)
+    _check(load().moe_unpack4(_ptr(q4), _ptr(s4), E, Kd, N, _ptr(w), _handle(stream, dev)))
     return w
 
 
 def moe_grouped_gemm4_swiglu(x, src, K, gate, up, offsets, cap_rows, h=None, stream=None):
     """Gate/up product and SwiGLU on 4-bit weights (gate, up: (q4, s4) pairs), row r from x[src[r] // K], or
     from x[r] if src is None (rows already in expert order; K unused)."""
-    _need(x, torch.bfloat16, "x")
-    _need(offsets, torch.int32, "offsets")
+    dev = _device(stream, x)
+    _arg(x, torch.bfloat16, "x", dev)
     if x.dim() != 2:
         raise MoeError(f"x: expected [T, H], got {tuple(x.shape)}")
     T, H = x.shape
-    gq, gs, EL, F = _weights4(gate, H, "gate")
-    uq, us, _, _ = _weights4(up, H, "up", EL, F)
-    if offsets.numel() < EL + 1:
-        raise MoeError(f"offsets: expected {EL + 1} entries, got {offsets.numel()}")
+    gq, gs, EL, F = _weights4(gate, H, "gate", dev)
+    uq, us, _, _ = _weights4(up, H, "up", dev, EL, F)
+    _offsets(offsets, EL, dev)
     if src is None:
         _rows(x, cap_rows, H, "x")
     else:
-        _need(src, torch.int32, "src")
+        _arg(src, torch.int32, "src", dev)
         if src.numel() < cap_rows:
             raise MoeError(f"src: expected at least {cap_rows} entries, got {src.numel()}")
-    if h is None:
-        h = torch.empty((max(cap_rows, 1), F), dtype=torch.bfloat16, device=x.device)
-    _need(h, torch.bfloat16, "h")
-    _rows(h, cap_rows, F, "h")
+    n = max(cap_rows, 0)
+    h = _out(h, (n, F), torch.bfloat16, "h", dev, n)
     _check(load().moe_grouped_gemm4_swiglu(_ptr(x), T, _ptr(src), int(K or 0), _ptr(gq), _ptr(gs), _ptr(uq),
                                            _ptr(us), _ptr(offsets), EL, H, F, cap_rows, _ptr(h),
-                                           _on_device(stream, x, src, gq, gs, uq, us, offsets, h)))
+                                           _handle(stream, dev)))
     return h
 
 
 def moe_grouped_gemm4(a, w, offsets, cap_rows, c=None, stream=None):
     """c[r] = a[r] . w_j on 4-bit weights w = (q4, s4); rows in expert order."""
-    _need(a, torch.bfloat16, "a")
-    _need(offsets, torch.int32, "offsets")
+    dev = _device(stream, a)
+    _arg(a, torch.bfloat16, "a", dev)
     if a.dim() != 2 or a.shape[0] < cap_rows:
         raise MoeError(f"a: expected at least {cap_rows} rows, got {tuple(a.shape)}")
     Kd = a.shape[1]
-    q4, s4, EL, N = _weights4(w, Kd, "w")
-    if offsets.numel() < EL + 1:
-        raise MoeError(f"offsets: expected {EL + 1} entries, got {offsets.numel()}")
-    if c is None:
-        c = torch.empty((max(cap_rows, 1), N), dtype=torch.bfloat16, device=a.device)
-    _need(c, torch.bfloat16, "c")
-    _rows(c, cap_rows, N, "c")
+    q4, s4, EL, N = _weights4(w, Kd, "w", dev)
+    _offsets(offsets, EL, dev)
+    n = max(cap_rows, 0)
+    c = _out(c, (n, N), torch.bfloat16, "c", dev, n)
     _check(load().moe_grouped_gemm4(_ptr(a), _ptr(q4), _ptr(s4), _ptr(offsets), EL, Kd, N, cap_rows, _ptr(c),
-                                    _on_device(stream, a, q4, s4, offsets, c)))
+                                    _handle(stream, dev)))
     return c
 
 
@@ -773,34 +771,29 @@ def moe_gemm4_combine_workspace_size(cap_rows, N) -> int:
 def moe_grouped_gemm4_combine(a, w, offsets, cap_rows, pos, gates, y=None, out=None, ws=None, stream=None):
     """out[t] = sum_k gates[t,k] * (a[pos[t,k]] . w) on 4-bit weights, the experts' rows kept in fp32 (ws) until
     the one rounding of out; y (optional): those rows in bf16, as moe_grouped_gemm4 gives them."""
-    _need(a, torch.bfloat16, "a")
-    _need(offsets, torch.int32, "offsets")
-    _need(pos, torch.int32, "pos")
-    _need(gates, torch.float32, "gates")
+    dev = _device(stream, a)
+    _arg(a, torch.bfloat16, "a", dev)
+    _arg(pos, torch.int32, "pos", dev)
+    _arg(gates, torch.float32, "gates", dev)
     if a.dim() != 2 or a.shape[0] < cap_rows:
         raise MoeError(f"a: expected at least {cap_rows} rows, got {tuple(a.shape)}")
-    Kd = a.shape[1]
-    q4, s4, EL, N = _weights4(w, Kd, "w")
-    if offsets.numel() < EL + 1:
-        raise MoeError(f"offsets: expected {EL + 1} entries, got {offsets.numel()}")
     if pos.dim() != 2:
         raise MoeError(f"pos: expected [T, K], got {tuple(pos.shape)}")
-    T, K = pos.shape
+    Kd, (T, K) = a.shape[1], pos.shape
+    q4, s4, EL, N = _weights4(w, Kd, "w", dev)
+    _offsets(offsets, EL, dev)
     _shape(gates, (T, K), "gates")
     if y is not None:
-        _need(y, torch.bfloat16, "y")
+        _arg(y, torch.bfloat16, "y", dev)
         _rows(y, cap_rows, N, "y")
-    if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=a.device)
-    _need(out, torch.bfloat16, "out")
-    _shape(out, (T, N), "out")
+    out = _out(out, (T, N), torch.bfloat16, "out", dev)
     need = moe_gemm4_combine_workspace_size(cap_rows, N)
     if ws is None or ws.numel() < need:
         ws = torch.empty(max(need, 256), dtype=torch.uint8, device=a.device)
-    _need(ws, torch.uint8, "ws")
+    _arg(ws, torch.uint8, "ws", dev)
     _check(load().moe_grouped_gemm4_combine(_ptr(a), _ptr(q4), _ptr(s4), _ptr(offsets), EL, Kd, N, cap_rows,
                                             _ptr(pos), _ptr(gates), T, K, _ptr(y), _ptr(out), _ptr(ws), ws.numel(),
-                                            _on_device(stream, a, q4, s4, offsets, pos, gates, y, out, ws)))
+                                            _handle(stream, dev)))
     return out
 
 
