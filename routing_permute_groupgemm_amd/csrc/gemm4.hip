@@ -51,8 +51,16 @@ struct Gemm4Params {
 constexpr uint32_t kNoRow = kOOB_GATHER;
 
 // The tile of this workgroup, the same in every lane (j = -1: none).  Lane l
-// holds the row tiles of experts l*PER .. l*PER+PER-1.
-template <int PER, int BM>
+// holds the row tiles of experts l*PER .. l*PER+PER-1.  Workgroup b runs on XCD
+// b % 8, and each XCD takes a contiguous run of the order:
+//   BY_EXPERT  an expert's slabs (blocks of columns) one after another, the row
+//              tiles of a slab next to each other: they read the same weights, and
+//              the slabs the same rows, through one L2 (256 tokens: down 51 against 52
+//              us, gate/up 80 against 82);
+//   otherwise  the row tiles of all experts, slab by slab: with one or two rows an
+//              expert there is nothing to share, and a run over all experts was
+//              faster (one token: gate/up 12.0 against 12.8 us).
+template <int PER, int BM, bool BY_EXPERT>
 __device__ __forceinline__ void find_tile(const Gemm4Params& p, int lane, int slabs, int& j, int& row0, int& rows,
                                           int& slab) {
     int at[PER + 1];
@@ -72,29 +80,52 @@ __device__ __forceinline__ void find_tile(const Gemm4Params& p, int lane, int sl
         const int t = __shfl_up(incl, o, 64);
         if (lane >= o) incl += t;
     }
-    const int tiles = __builtin_amdgcn_readlane(incl, 63);
-    // workgroup b runs on XCD b % 8: each XCD takes a contiguous run, in which
-    // an expert's row tiles of one slab (the same weights) are neighbours
-    const int run = (tiles * slabs + 7) >> 3;
+    const int total = __builtin_amdgcn_readlane(incl, 63);
+    const int run = (total * slabs + 7) >> 3;
     const int b = (int)(blockIdx.x >> 3);
-    const int id = (int)(blockIdx.x & 7) * run + b;
-    if (b >= run || id >= tiles * slabs) return;
-    slab = id / tiles;
-    const int tile = id - slab * tiles;
-    const int owner = __builtin_ctzll(__ballot(incl > tile));  // the first lane with more tiles up to it
-    int rest = tile - (incl - mine), jj = 0, r0 = 0, end = 0;
+    int id = (int)(blockIdx.x & 7) * run + b;
+    if (b >= run || id >= total * slabs) return;
+    const int per = BY_EXPERT ? slabs : 1;  // places of a row tile in the order searched here
+    if (!BY_EXPERT) {
+        slab = id / total;
+        id -= slab * total;
+    }
+    const int owner = __builtin_ctzll(__ballot(incl * per > id));  // the first lane with more places up to it
+    int rest = id - (incl - mine) * per, expert = 0, place = 0, tiles = 1, first = 0, end = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        if (rest >= 0 && rest < n[i]) {
-            jj = lane * PER + i;
-            r0 = at[i] + rest * BM;
+        if (rest >= 0 && rest < n[i] * per) {
+            expert = lane * PER + i;
+            place = rest;
+            tiles = n[i];
+            first = at[i];
             end = at[i + 1];
         }
-        rest -= n[i];
+        rest -= n[i] * per;
     }
-    j = __builtin_amdgcn_readlane(jj, owner);
-    row0 = __builtin_amdgcn_readlane(r0, owner);
+    j = __builtin_amdgcn_readlane(expert, owner);
+    place = __builtin_amdgcn_readlane(place, owner);
+    if (BY_EXPERT) {
+        tiles = __builtin_amdgcn_readlane(tiles, owner);
+        slab = place;
+        place = 0;
+        if (tiles > 1) {
+            place = slab % tiles;
+            slab /= tiles;
+        }
+    }
+    row0 = __builtin_amdgcn_readlane(first, owner) + place * BM;
     rows = min(BM, __builtin_amdgcn_readlane(end, owner) - row0);
+}
+
+template <int BM, bool BY_EXPERT>
+__device__ __forceinline__ void find_tile_of(const Gemm4Params& p, int lane, int slabs, int& j, int& row0, int& rows,
+                                             int& slab) {
+    j = -1;
+    if (p.e_local <= 64) find_tile<1, BM, BY_EXPERT>(p, lane, slabs, j, row0, rows, slab);
+    else if (p.e_local <= 128) find_tile<2, BM, BY_EXPERT>(p, lane, slabs, j, row0, rows, slab);
+    else if (p.e_local <= 256) find_tile<4, BM, BY_EXPERT>(p, lane, slabs, j, row0, rows, slab);
+    else find_tile<8, BM, BY_EXPERT>(p, lane, slabs, j, row0, rows, slab);
 }
 
 // 4 x 4 transpose between register index and lane group of 16 (16 bytes each):
@@ -111,16 +142,6 @@ __device__ __forceinline__ void transpose4(u32x4 (&v)[4]) {
         v[2][i] = d[0];
         v[3][i] = d[1];
     }
-}
-
-template <int BM>
-__device__ __forceinline__ void find_tile_of(const Gemm4Params& p, int lane, int slabs, int& j, int& row0, int& rows,
-                                             int& slab) {
-    j = -1;
-    if (p.e_local <= 64) find_tile<1, BM>(p, lane, slabs, j, row0, rows, slab);
-    else if (p.e_local <= 128) find_tile<2, BM>(p, lane, slabs, j, row0, rows, slab);
-    else if (p.e_local <= 256) find_tile<4, BM>(p, lane, slabs, j, row0, rows, slab);
-    else find_tile<8, BM>(p, lane, slabs, j, row0, rows, slab);
 }
 
 // The resource that a tile's rows are read through (rows past it read 0), and
@@ -204,7 +225,7 @@ __global__ __launch_bounds__(64 * W) void gemm4_split(Gemm4Params p) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int slabs = (p.N / 16 + NT - 1) / NT;
     int j, row0, rows, slab;
-    find_tile_of<16>(p, lane, slabs, j, row0, rows, slab);
+    find_tile_of<16, false>(p, lane, slabs, j, row0, rows, slab);
     if (j < 0) return;
     const int nt0 = slab * NT, r16 = lane & 15, g = lane >> 4;
 
@@ -297,7 +318,7 @@ __global__ __launch_bounds__(64 * W) void gemm4_wide(Gemm4Params p) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int slabs = (p.N / 16 + NT * W - 1) / (NT * W);
     int j, row0, rows, slab;
-    find_tile_of<16 * MT>(p, lane, slabs, j, row0, rows, slab);
+    find_tile_of<16 * MT, true>(p, lane, slabs, j, row0, rows, slab);
     if (j < 0) return;
     const int nt0 = (slab * W + wave) * NT, r16 = lane & 15, g = lane >> 4;
 
