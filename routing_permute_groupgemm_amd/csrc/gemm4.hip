@@ -24,7 +24,7 @@
 //     every SIMD a wave of its own columns.
 //   gemm4_wide: every wave has its own 16*NT columns and runs the whole
 //     contraction; the rows, which the waves share, go through LDS.  Nothing is
-//     reduced across waves, and a row byte is read once per 64*NT columns.
+//     reduced across waves, and a row byte is read once per workgroup.
 // The rule between them is in launch4_rows.
 #include "mx.hpp"
 
@@ -427,13 +427,19 @@ static int launch_wide(const Gemm4Params& p, hipStream_t s) {
 //     make 512 workgroups, two a CU (gate/up of two tokens 19.9 against 22.9 us, of
 //     one 12.8 against 11.7).
 //   wide: row tiles of 16, or of 32 when there are more than 16 rows an expert
-//     (gate/up of 512 tokens, 128 experts: 183 against 207 us; 64 rows took 186 to 220).
+//     (gate/up of 512 tokens, 128 experts: 173 against 202 us; 64 rows took 182 to 218;
+//     23 tokens, one or two rows an expert: 30 with 16 rows, 32 with 32).
 //   non-temporal weights: when the packed matrices that the rows can touch
 //     fill half the last-level cache (128 MB) or more, so that they are not there the
 //     next time, and an expert's rows mostly fit one tile (three quarters of it or
 //     less on average), so that no other workgroup reads them again.  Gate/up of 256
-//     tokens on 32 experts 82 against 90 us; of 512 on 128 experts, whose larger ones
-//     take three tiles, 190 against 183.
+//     tokens on 32 experts 77 against 90 us; of 512 on 128 experts, whose larger ones
+//     take three tiles, 189 against 173.
+//
+// What bounds them is the stream of weights.  512 tokens: gate/up fetches 0.92 GB (of
+// 0.89 that it must) and down 0.45 (0.44) at about 5.2 TB/s, near what a plain copy
+// reaches without the non-temporal hint (5.4); with the conversions or the matrix
+// instructions left out they took as long.  256 tokens, non-temporal: 6.5 TB/s.
 template <int MATS>
 static int launch4_rows(const Gemm4Params& p, hipStream_t s) {
     const int64_t cols = p.N / 16;
@@ -453,12 +459,14 @@ static int launch4_rows(const Gemm4Params& p, hipStream_t s) {
         return launch_wide<MATS, 2, 1, 8, false>(p, s);
     }
     // several row tiles an expert: 256 columns a workgroup, so that the rows are read half as often (512
-    // tokens: gate/up 179 against 183 us, down 108 against 126; 2048 tokens: 428 against 462 and 269 against 342)
+    // tokens: gate/up 173 against 175 us, down 106 against 119; 2048 tokens: 415 against 435 and 255 against 318)
     return launch_wide<MATS, 2, 2, 8, false>(p, s);
 }
 
 // out[t] = bf16(sum over k ascending of gate[t,k] * y[pos[t,k]]) from fp32 rows: moe_combine without the rounding
-// of y.  4 columns per thread; a token's rows and gates are the same in every lane of a wave.
+// of y, which left out 2.9e-3 off where it is 2.4e-3 off now (the bf16 of h and of out remain).  4 columns per
+// thread; a token's rows and gates are the same in every lane of a wave.  Bound by the rows' bytes (512 tokens,
+// H = 4096: 12 us for 71 MB), for a token or two by its latency (4 us).
 __global__ __launch_bounds__(256) void combine32_kernel(const float* __restrict__ y, int64_t cap,
                                                         const int32_t* __restrict__ pos,
                                                         const float* __restrict__ gates, int T, int K, int N,

@@ -10,6 +10,9 @@
 // performance model notes that SwiGLU is purely memory-bound, so it is fused
 // into the GEMM epilogue.
 //
+// The SwiGLU epilogues also come in 8-bit forms, which save (a, b) for the
+// backward, and read it there, in block-scaled bytes (mx.hpp).
+//
 // One kernel template covers every GEMM of the layer:
 //   ROWS schedule  C[r, :] = A[r, :] . B_j for the rows r of expert j
 //     A (x_perm, h, dy_perm, dab) is contraction-contiguous ("KC");
@@ -1032,7 +1035,9 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
                 // XOR-swizzled by row pair.  Each lane reads the four bytes of its
                 // MFMA-layout columns and widens them there, with the scales of its own
                 // row; (da, db) and then h go out as whole 256-byte row pieces through the
-                // same 8 KiB.
+                // same 8 KiB.  T = 16384, H = 2048, F = 768: 558 us (606 with the bytes widened
+                // before they are staged); T = 131072, H = 7168, F = 2048: 3.65 ms; the bf16
+                // epilogue, which reads twice the bytes and does not write h, 532 us and 3.52.
                 static_assert(TL::kStage / TL::kWaves >= 8192 && BN / WN == 128, "staging space per wave");
                 uint8_t* stg = smem + ((gs + S - 1) % S) * TL::kStage + wave * 8192;
                 const int ln = lane_id_here();
@@ -1478,6 +1483,9 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
             // rows, and the tile's h and ab stores took about twice as long.  The
             // gathered-row bodies keep the direct stores: their extra per-lane row
             // offsets leave no registers for the staged form, which spilled there.
+            // The 8-bit save is staged there too (53 registers spilled, 284 with the
+            // direct form): 6.58 ms against 6.89 with the bf16 save at T = 131072, 0.91
+            // against 0.95 at 16384.
             constexpr int kBufs = TL::kStage / TL::kWaves >= 8192 ? 2 : 1;
             uint8_t* stg = smem + ((gs + S - 1) % S) * TL::kStage + wave * (kBufs * 4096);
             const int ln = lane_id_here();
@@ -1498,7 +1506,13 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
                 }
             };
             // the staged a or b rows (32 bf16 of a block in 4 lanes) as 8-bit blocks: 64
-            // bytes of a row per 8 lanes, and its two scale bytes
+            // bytes of a row per 8 lanes, and its two scale bytes.  About 45 vector
+            // instructions per 8 values, for half the bytes that the bf16 rows take: the
+            // GEMM with it runs 0.9% longer than with the bf16 save (T = 131072, H = 7168,
+            // F = 2048: 6.45 against 6.39 ms; T = 16384, H = 2048, F = 768: 0.89 against
+            // 0.86), where a pass of its own over the saved rows takes 0.24 ms.  Packed
+            // straight from the MFMA layout (a block in lanes l and l ^ 32) the 256-row
+            // body spilled 254 registers.
             auto flush8 = [&](int buf, int mt, int half) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -1606,7 +1620,7 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
                     }
                 }
             } else if constexpr (EPI == EPI_SWIGLU8) {
-                // a 32-column block of a row is in lanes l and l ^ 32
+                // the small bodies; a 32-column block of a row is in lanes l and l ^ 32
 #pragma unroll
                 for (int i2 = 0; i2 < NTW / 2; ++i2) {
                     const f32x16& ga = acc[mt][i2];

@@ -330,7 +330,9 @@ COUNTS = {
     "none": [0, 0, 0],
     "many": [70, 129, 0, 64, 200],
     "last_only": [0] * 130 + [5],
+    "hundred": [(5 * i) % 3 for i in range(100)],
     "wide": [(7 * i) % 4 for i in range(300)],
+    "most_experts": [(i % 9 == 4) * 2 for i in range(512)],
 }
 
 
@@ -350,7 +352,7 @@ def check_combined(got, pos, gates, y, ey):
 @pytest.mark.parametrize("counts", list(COUNTS))
 def test_gemm4_against_float64(counts, H, F):
     n = COUNTS[counts]
-    if len(n) > 100 and H * F > 128 * 192:
+    if len(n) >= 100 and H * F > 128 * 192:
         H, F = 64, 128
     if H * F > 1408 * 320 and counts not in ("wide_rows", "even", "tens"):
         H, F = 64, 1088
@@ -496,6 +498,116 @@ def test_binding_refuses_wrong_shapes():
     ):
         with pytest.raises(_lib.MoeError):
             call()
+
+
+def test_nothing_to_do():
+    """No expert, no row, no token: nothing is written, and the combined sum of no rows is 0."""
+    dev = "cuda"
+    q4, s4 = _lib.moe_pack4(torch.zeros((0, 64, 64), dtype=torch.bfloat16, device=dev))
+    assert q4.shape == (0, 4, 1, 64, 16) and s4.shape == (0, 4, 1, 64)
+    offsets = torch.zeros(1, dtype=torch.int32, device=dev)
+    x = torch.ones((5, 64), dtype=torch.bfloat16, device=dev)
+    src = torch.zeros(3, dtype=torch.int32, device=dev)
+    h = torch.full((3, 64), 5.0, dtype=torch.bfloat16, device=dev)
+    _lib.moe_grouped_gemm4_swiglu(x, src, 1, (q4, s4), (q4, s4), offsets, 3, h=h)
+    _lib.moe_grouped_gemm4(x, (q4, s4), offsets, 3, c=h)
+    assert (h == 5.0).all()
+    w = _lib.moe_pack4(torch.ones((2, 64, 64), dtype=torch.bfloat16, device=dev))
+    off2 = torch.tensor([0, 0, 0], dtype=torch.int32, device=dev)
+    for weights, off, cap in (((q4, s4), offsets, 3), (w, off2, 3), (w, off2, 0)):
+        out = torch.full((5, 64), 5.0, dtype=torch.bfloat16, device=dev)
+        _lib.moe_grouped_gemm4_combine(x, weights, off, cap, torch.full((5, 2), -1, dtype=torch.int32, device=dev),
+                                       torch.ones((5, 2), device=dev), out=out)
+        assert (out == 0).all()
+    assert _lib.moe_grouped_gemm4(x, w, off2, 0).shape == (0, 64)
+    q, s = _lib.moe_pack8(torch.zeros((0, 64), dtype=torch.bfloat16, device=dev))
+    assert _lib.moe_unpack8(q, s).shape == (0, 64)
+    wb = torch.zeros((2, 64, 64), dtype=torch.bfloat16, device=dev)
+    assert _lib.moe_grouped_gemm_swiglu_save8(x, wb, wb, off2, 0)[1].shape == (0, 128)
+    assert _lib.moe_grouped_gemm_swiglu_bwd8(x, wb, off2, 0, q.new_empty((0, 128)), s.new_empty((0, 4)))[0].shape == (0, 128)
+
+
+def test_buffers_past_2_31_elements():
+    """262 300 rows: the 8192 bytes of a row's (a, b) and the fp32 and bf16 rows of the products lie on both sides of
+    2 and 4 GiB.  Rows there equal those of a call on them alone (h and the bytes bit for bit, the rest within its
+    tolerance against float64)."""
+    rows, H, F = 262300, 64, 4096
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(50)
+    x = torch.randn((rows, H), generator=gen, device="cuda").to(torch.bfloat16)
+    w = [(torch.randn((1, H, F), generator=gen, device="cuda") * 0.1).to(torch.bfloat16) for _ in range(2)]
+    offsets = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    at = torch.tensor([0, 131071, 131072, 262143, 262144, 262145, rows - 1], device="cuda")
+    few = torch.tensor([0, at.numel()], dtype=torch.int32, device="cuda")
+    print("[mx] large save8", flush=True)
+    h, q, s = _lib.moe_grouped_gemm_swiglu_save8(x, w[0], w[1], offsets, rows)
+    h1, q1, s1 = _lib.moe_grouped_gemm_swiglu_save8(x[at], w[0], w[1], few, at.numel())
+    for a, b in ((h, h1), (q, q1), (s, s1)):
+        assert torch.equal(a[at], b)
+    assert torch.equal(_lib.moe_unpack8(q, s)[at], _lib.moe_unpack8(q1, s1))
+    print("[mx] large bwd8", flush=True)
+    wd = (torch.randn((1, F, H), generator=gen, device="cuda") * 0.1).to(torch.bfloat16)
+    dab, h = _lib.moe_grouped_gemm_swiglu_bwd8(x, wd, offsets, rows, q, s)
+    wdab, tol, wh, htol = bwd_reference(mx_ref.f64(bits(x[at])), mx_ref.f64(bits(wd)),
+                                        mx_ref.f64(bits(_lib.moe_unpack8(q1, s1))), bits(few), at.numel())
+    within("dab", bits(dab[at]), wdab, tol)
+    within("h", bits(h[at]), wh, htol)
+    del dab, q, s
+    print("[mx] large 4-bit", flush=True)
+    packed = [_lib.moe_pack4(m) for m in w]
+    vals = [mx_ref.f64(bits(_lib.moe_unpack4(*p, H)))[0] for p in packed]
+    xr = mx_ref.f64(bits(x[at]))
+    c = _lib.moe_grouped_gemm4(torch.cat((x, x)), packed[0], 2 * offsets, 2 * rows)
+    for half in (0, rows):
+        want, mag = xr @ vals[0], np.abs(xr) @ np.abs(vals[0])
+        within("c", bits(c[at + half]), want, H * U32 * mag + UBF * np.abs(want) + 1e-37)
+    del c
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda").flip(0).reshape(-1, 2).contiguous()
+    gates = torch.rand(pos.shape, generator=gen, device="cuda")
+    out = _lib.moe_grouped_gemm4_combine(x, packed[0], offsets, rows, pos, gates)
+    t = [0, 1, 65535, 65536, 131149]
+    for i in t:
+        g, p = bits(gates)[i].astype(np.float64), bits(pos)[i]
+        xr = mx_ref.f64(bits(x[torch.from_numpy(p).cuda().long()]))
+        r = xr @ vals[0]
+        mag = H * U32 * (np.abs(xr) @ np.abs(vals[0])) + 4 * U32 * np.abs(r)
+        want = (g[:, None] * r).sum(0)
+        within("out", bits(out[i]), want, (g[:, None] * mag).sum(0) + UBF * np.abs(want) + 1e-37)
+
+
+def test_two_streams_at_once():
+    """The same calls on two streams with buffers of their own: each gives the bits that it gives alone."""
+    shape = SHAPES["ep_share_small"]
+    inp, dev, buf, R = routed(shape, 26, backward=True)
+    ab = dev16(normal((buf.cap, 2 * shape.F), 51, 2.0))
+    packed = {k: _lib.moe_pack4(dev[k]) for k in ("w_gate", "w_up", "w_down")}
+
+    def chain():
+        h, q, s = _lib.moe_grouped_gemm_swiglu_save8(buf.x_perm, dev["w_gate"], dev["w_up"], buf.offsets, buf.cap)
+        dab, h2 = _lib.moe_grouped_gemm_swiglu_bwd8(buf.x_perm, dev["w_down"], buf.offsets, buf.cap, q, s)
+        h4 = _lib.moe_grouped_gemm4_swiglu(dev["x"], buf.src, shape.K, packed["w_gate"], packed["w_up"], buf.offsets,
+                                           buf.cap)
+        out = _lib.moe_grouped_gemm4_combine(h4, packed["w_down"], buf.offsets, buf.cap, buf.pos, buf.gates)
+        p, ps = _lib.moe_pack8(ab)
+        return [h[:R], q[:R], s[:R], dab[:R], h2[:R], h4[:R], out, p, ps]
+
+    want = [t.clone() for t in chain()]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(chain())
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, want))
+    # and by argument instead of the current stream
+    q, s = _lib.moe_pack8(ab, stream=streams[0])
+    streams[0].synchronize()
+    assert torch.equal(q, want[7]) and torch.equal(s, want[8])
 
 
 # ---- together, as the pipeline runs them ----------------------------------------------------------------------
