@@ -787,10 +787,11 @@ def moe_grouped_gemm4_combine(a, w, offsets, cap_rows, pos, gates, y=None, out=N
         _arg(y, torch.bfloat16, "y", dev)
         _rows(y, cap_rows, N, "y")
     out = _out(out, (T, N), torch.bfloat16, "out", dev)
-    need = moe_gemm4_combine_workspace_size(cap_rows, N)
+    if ws is not None:
+        _arg(ws, torch.uint8, "ws", dev)
+    need = 4 * max(cap_rows, 0) * N  # as the library's own size, without a call
     if ws is None or ws.numel() < need:
         ws = torch.empty(max(need, 256), dtype=torch.uint8, device=a.device)
-    _arg(ws, torch.uint8, "ws", dev)
     _check(load().moe_grouped_gemm4_combine(_ptr(a), _ptr(q4), _ptr(s4), _ptr(offsets), EL, Kd, N, cap_rows,
                                             _ptr(pos), _ptr(gates), T, K, _ptr(y), _ptr(out), _ptr(ws), ws.numel(),
                                             _handle(stream, dev)))

@@ -420,12 +420,11 @@ static int launch_wide(const Gemm4Params& p, hipStream_t s) {
 
 // Which kernel, from the host's sizes alone: cap rows over e_local experts make at
 // most `tiles` row tiles of 16.
-//   split: fewer than 3 waves a SIMD (3072) if every wave took 16 columns.
-//     One token, H = 4096, F = 1536, gate/up (768): 11.7 us against 16.5 us;
-//     four tokens (3072): 36.8 against 34.4.  Down, one token (2048): 7.4 against
-//     8.0; two (4096): 11.9 against 10.7.  Two column tiles a workgroup once those
-//     make 512 workgroups, two a CU (gate/up of two tokens 19.9 against 22.9 us, of
-//     one 12.8 against 11.7).
+//   split: fewer than 3 waves a SIMD if every wave took 16 columns.  One token, H =
+//     4096, F = 1536, gate/up (0.75 waves a SIMD): 11.7 us against 16.5; four tokens
+//     (3): 36.8 against 34.4.  Down, one token (2): 7.4 against 8.0; two (4): 11.9
+//     against 10.7.  Two column tiles a workgroup once those make two workgroups a
+//     CU (gate/up of two tokens 19.9 against 22.9 us, of one 12.8 against 11.7).
 //   wide: row tiles of 16, or of 32 when there are more than 16 rows an expert
 //     (gate/up of 512 tokens, 128 experts: 173 against 202 us; 64 rows took 182 to 218;
 //     23 tokens, one or two rows an expert: 30 with 16 rows, 32 with 32).
@@ -444,8 +443,9 @@ template <int MATS>
 static int launch4_rows(const Gemm4Params& p, hipStream_t s) {
     const int64_t cols = p.N / 16;
     const int64_t tiles = std::min<int64_t>(p.cap, p.cap / 16 + p.e_local);
-    if (tiles * cols < 3072) {
-        if (tiles * cols >= 1024) return launch_split<MATS, 2, 4>(p, s);
+    const int64_t cus = moe_host::num_cus();
+    if (tiles * cols < 3 * 4 * cus) {
+        if (tiles * cols >= 2 * 2 * cus) return launch_split<MATS, 2, 4>(p, s);
         return launch_split<MATS, 1, 4>(p, s);
     }
     const int64_t experts = std::min<int64_t>(p.cap, p.e_local);

@@ -128,6 +128,8 @@ def combine(buf: MoeBuffers):
 
 def forward(buf: MoeBuffers, inp: dict):
     """inp: device tensors logits, x, w_gate, w_up, w_down."""
+    if buf.weights4:
+        raise _lib.MoeError("forward: these buffers are for 4-bit weights (forward4)")
     route(buf, inp["logits"])
     permute(buf, inp["x"])
     expert_up(buf, inp["w_gate"], inp["w_up"], inp["x"])

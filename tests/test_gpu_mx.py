@@ -677,6 +677,8 @@ def test_decode_step_on_4bit_weights(name, T):
     check_combined(bits(buf.out), bits(buf.pos), bits(buf.gates), y, ey)
     with pytest.raises(_lib.MoeError):
         pipeline.forward4(ref, dev)
+    with pytest.raises(_lib.MoeError):
+        pipeline.forward(buf, dev)
 
 
 def test_replay_from_a_graph_and_another_stream():
