@@ -484,7 +484,8 @@ int moe_grouped_gemm4(const moe_bf16* a, const uint8_t* q4, const uint8_t* s4, c
  * to bf16.
  *   pos int32 [T,K], gates fp32 [T,K];  y bf16 [cap_rows,N] or NULL;  out bf16 [T,N];
  *   ws: device workspace of at least moe_gemm4_combine_workspace_size(cap_rows, N)
- *   bytes (the fp32 rows).  T <= 262140; MOE_EWORKSPACE if ws is NULL or too small.
+ *   bytes (the fp32 rows), one for each of calls that may overlap.  T <= 262140;
+ *   MOE_EWORKSPACE if ws is NULL or too small.
  */
 size_t moe_gemm4_combine_workspace_size(int cap_rows, int N);
 int moe_grouped_gemm4_combine(const moe_bf16* a, const uint8_t* q4, const uint8_t* s4, const int32_t* offsets,

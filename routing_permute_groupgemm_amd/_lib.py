@@ -575,7 +575,7 @@ def _offsets(offsets, EL, dev):
 def _out(t, shape, dtype, name, dev, rows=None):
     """The caller's buffer (checked: at least `rows` rows, or exactly `shape`) or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
+        return torch.empty(shape, dtype=dtype, device=dev)
     _arg(t, dtype, name, dev)
     if rows is None:
         _shape(t, shape, name)
