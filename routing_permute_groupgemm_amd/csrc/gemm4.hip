@@ -44,15 +44,17 @@ struct Gemm4Params {
     int Kd, N, KT;
     uint16_t* c;         // bf16 [cap, N], or NULL
     float* c32;          // fp32 [cap, N], or NULL
+    bool stream;         // weights that one row tile reads carry the non-temporal hint (launch4_rows)
 };
 
 // Per-lane byte offset that is outside every resource (those of tokens may
 // reach 3.75 GiB), also with any column offset of a row added.
 constexpr uint32_t kNoRow = kOOB_GATHER;
 
-// The tile of this workgroup, the same in every lane (j = -1: none).  Lane l
-// holds the row tiles of experts l*PER .. l*PER+PER-1.  Workgroup b runs on XCD
-// b % 8, and each XCD takes a contiguous run of the order:
+// The tile of this workgroup, the same in every lane (j = -1: none), and the number
+// of row tiles of its expert (`tiles`).  Lane l holds the row tiles of experts
+// l*PER .. l*PER+PER-1.  Workgroup b runs on XCD b % 8, and each XCD takes a
+// contiguous run of the order:
 //   BY_EXPERT  an expert's slabs (blocks of columns) one after another, the row
 //              tiles of a slab next to each other: they read the same weights, and
 //              the slabs the same rows, through one L2 (256 tokens: down 51 against 52
@@ -62,7 +64,7 @@ constexpr uint32_t kNoRow = kOOB_GATHER;
 //              faster (one token: gate/up 12.0 against 12.8 us).
 template <int PER, int BM, bool BY_EXPERT>
 __device__ __forceinline__ void find_tile(const Gemm4Params& p, int lane, int slabs, int& j, int& row0, int& rows,
-                                          int& slab) {
+                                          int& slab, int& tiles) {
     int at[PER + 1];
 #pragma unroll
     for (int i = 0; i <= PER; ++i) at[i] = p.offsets[min(lane * PER + i, p.e_local)];
@@ -91,13 +93,13 @@ __device__ __forceinline__ void find_tile(const Gemm4Params& p, int lane, int sl
         id -= slab * total;
     }
     const int owner = __builtin_ctzll(__ballot(incl * per > id));  // the first lane with more places up to it
-    int rest = id - (incl - mine) * per, expert = 0, place = 0, tiles = 1, first = 0, end = 0;
+    int rest = id - (incl - mine) * per, expert = 0, place = 0, count = 1, first = 0, end = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         if (rest >= 0 && rest < n[i] * per) {
             expert = lane * PER + i;
             place = rest;
-            tiles = n[i];
+            count = n[i];
             first = at[i];
             end = at[i + 1];
         }
@@ -105,8 +107,8 @@ __device__ __forceinline__ void find_tile(const Gemm4Params& p, int lane, int sl
     }
     j = __builtin_amdgcn_readlane(expert, owner);
     place = __builtin_amdgcn_readlane(place, owner);
+    tiles = __builtin_amdgcn_readlane(count, owner);
     if (BY_EXPERT) {
-        tiles = __builtin_amdgcn_readlane(tiles, owner);
         slab = place;
         place = 0;
         if (tiles > 1) {
@@ -120,12 +122,12 @@ __device__ __forceinline__ void find_tile(const Gemm4Params& p, int lane, int sl
 
 template <int BM, bool BY_EXPERT>
 __device__ __forceinline__ void find_tile_of(const Gemm4Params& p, int lane, int slabs, int& j, int& row0, int& rows,
-                                             int& slab) {
+                                             int& slab, int& tiles) {
     j = -1;
-    if (p.e_local <= 64) find_tile<1, BM, BY_EXPERT>(p, lane, slabs, j, row0, rows, slab);
-    else if (p.e_local <= 128) find_tile<2, BM, BY_EXPERT>(p, lane, slabs, j, row0, rows, slab);
-    else if (p.e_local <= 256) find_tile<4, BM, BY_EXPERT>(p, lane, slabs, j, row0, rows, slab);
-    else find_tile<8, BM, BY_EXPERT>(p, lane, slabs, j, row0, rows, slab);
+    if (p.e_local <= 64) find_tile<1, BM, BY_EXPERT>(p, lane, slabs, j, row0, rows, slab, tiles);
+    else if (p.e_local <= 128) find_tile<2, BM, BY_EXPERT>(p, lane, slabs, j, row0, rows, slab, tiles);
+    else if (p.e_local <= 256) find_tile<4, BM, BY_EXPERT>(p, lane, slabs, j, row0, rows, slab, tiles);
+    else find_tile<8, BM, BY_EXPERT>(p, lane, slabs, j, row0, rows, slab, tiles);
 }
 
 // 4 x 4 transpose between register index and lane group of 16 (16 bytes each):
@@ -224,8 +226,8 @@ __global__ __launch_bounds__(64 * W) void gemm4_split(Gemm4Params p) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int slabs = (p.N / 16 + NT - 1) / NT;
-    int j, row0, rows, slab;
-    find_tile_of<16, false>(p, lane, slabs, j, row0, rows, slab);
+    int j, row0, rows, slab, shared;
+    find_tile_of<16, false>(p, lane, slabs, j, row0, rows, slab, shared);
     if (j < 0) return;
     const int nt0 = slab * NT, r16 = lane & 15, g = lane >> 4;
 
@@ -307,19 +309,15 @@ __global__ __launch_bounds__(64 * W) void gemm4_split(Gemm4Params p) {
 // tile are in flight while one is multiplied; deeper prefetch of the weights
 // (3 and 4 tiles) cost registers, and with them waves, and ran slower.  Row blocks
 // past the tile's rows are neither read nor multiplied.
-// NTL: the weights carry the non-temporal hint (see launch4_rows).
+// NTL: the weights carry the non-temporal hint.
 template <int MATS, int MT, int NT, int W, bool NTL>
-__global__ __launch_bounds__(64 * W) void gemm4_wide(Gemm4Params p) {
+__device__ __forceinline__ void wide_tile(const Gemm4Params& p, uint8_t (*xs)[MT * 4096], int j, int row0, int rows,
+                                          int slab) {
     // a thread's 16-byte loads of the rows per tile, and the rows that one of them covers
     constexpr int XL = MT * 4 / W, XR = 4 * W;
     static_assert(XL * W == MT * 4, "the rows' loads split evenly over the threads");
-    __shared__ __attribute__((aligned(16))) uint8_t xs[2][MT * 4096];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int slabs = (p.N / 16 + NT * W - 1) / (NT * W);
-    int j, row0, rows, slab;
-    find_tile_of<16 * MT, true>(p, lane, slabs, j, row0, rows, slab);
-    if (j < 0) return;
     const int nt0 = (slab * W + wave) * NT, r16 = lane & 15, g = lane >> 4;
 
     int64_t tiles[NT];
@@ -400,6 +398,20 @@ __global__ __launch_bounds__(64 * W) void gemm4_wide(Gemm4Params p) {
         }
 }
 
+template <int MATS, int MT, int NT, int W>
+__global__ __launch_bounds__(64 * W) void gemm4_wide(Gemm4Params p) {
+    __shared__ __attribute__((aligned(16))) uint8_t xs[2][MT * 4096];
+    const int slabs = (p.N / 16 + NT * W - 1) / (NT * W);
+    int j, row0, rows, slab, tiles;
+    find_tile_of<16 * MT, true>(p, threadIdx.x & 63, slabs, j, row0, rows, slab, tiles);
+    if (j < 0) return;
+    // An expert's weights that no other workgroup reads go past the cache; those of several row tiles stay in the L2
+    // that these share.  Gate/up of 256 tokens on 32 experts (one tile each) 77 against 90 us; of 512 tokens on 128
+    // experts (one to three) 170 against 189 with the hint on all and 175 on none.
+    if (p.stream && tiles == 1) wide_tile<MATS, MT, NT, W, true>(p, xs, j, row0, rows, slab);
+    else wide_tile<MATS, MT, NT, W, false>(p, xs, j, row0, rows, slab);
+}
+
 template <int MATS, int NT, int W>
 static int launch_split(const Gemm4Params& p, hipStream_t s) {
     const int64_t tiles = std::min<int64_t>(p.cap, p.cap / 16 + p.e_local);
@@ -409,12 +421,12 @@ static int launch_split(const Gemm4Params& p, hipStream_t s) {
     return moe_host::launch_status();
 }
 
-template <int MATS, int MT, int NT, int W, bool NTL>
+template <int MATS, int MT, int NT, int W>
 static int launch_wide(const Gemm4Params& p, hipStream_t s) {
     const int64_t tiles = std::min<int64_t>(p.cap, p.cap / (16 * MT) + p.e_local);
     const int64_t grid = (tiles * ((p.N / 16 + NT * W - 1) / (NT * W)) + 7) / 8 * 8;
     if (grid >= (1ll << 31)) return MOE_EINVAL;
-    gemm4_wide<MATS, MT, NT, W, NTL><<<(unsigned)grid, 64 * W, 0, s>>>(p);
+    gemm4_wide<MATS, MT, NT, W><<<(unsigned)grid, 64 * W, 0, s>>>(p);
     return moe_host::launch_status();
 }
 
@@ -428,19 +440,16 @@ static int launch_wide(const Gemm4Params& p, hipStream_t s) {
 //   wide: row tiles of 16, or of 32 when there are more than 16 rows an expert
 //     (gate/up of 512 tokens, 128 experts: 173 against 202 us; 64 rows took 182 to 218;
 //     23 tokens, one or two rows an expert: 30 with 16 rows, 32 with 32).
-//   non-temporal weights: when the packed matrices that the rows can touch
+//   non-temporal weights (stream): when the packed matrices that the rows can touch
 //     fill half the last-level cache (128 MB) or more, so that they are not there the
-//     next time, and an expert's rows mostly fit one tile (three quarters of it or
-//     less on average), so that no other workgroup reads them again.  Gate/up of 256
-//     tokens on 32 experts 77 against 90 us; of 512 on 128 experts, whose larger ones
-//     take three tiles, 189 against 173.
+//     next time, for the experts whose rows fit one tile (gemm4_wide).
 //
 // What bounds them is the stream of weights.  512 tokens: gate/up fetches 0.92 GB (of
 // 0.89 that it must) and down 0.45 (0.44) at about 5.2 TB/s, near what a plain copy
 // reaches without the non-temporal hint (5.4); with the conversions or the matrix
 // instructions left out they took as long.  256 tokens, non-temporal: 6.5 TB/s.
 template <int MATS>
-static int launch4_rows(const Gemm4Params& p, hipStream_t s) {
+static int launch4_rows(Gemm4Params p, hipStream_t s) {
     const int64_t cols = p.N / 16;
     const int64_t tiles = std::min<int64_t>(p.cap, p.cap / 16 + p.e_local);
     const int64_t cus = moe_host::num_cus();
@@ -449,18 +458,12 @@ static int launch4_rows(const Gemm4Params& p, hipStream_t s) {
         return launch_split<MATS, 1, 4>(p, s);
     }
     const int64_t experts = std::min<int64_t>(p.cap, p.e_local);
-    const bool large = experts * MATS * p.N * p.Kd * 17 / 32 >= (128ll << 20);
-    if (p.cap <= 16ll * p.e_local) {
-        if (large && p.cap <= 12ll * p.e_local) return launch_wide<MATS, 1, 2 / MATS, 4, true>(p, s);
-        return launch_wide<MATS, 1, 2 / MATS, 4, false>(p, s);
-    }
-    if (p.cap <= 24ll * p.e_local) {
-        if (large) return launch_wide<MATS, 2, 1, 8, true>(p, s);
-        return launch_wide<MATS, 2, 1, 8, false>(p, s);
-    }
+    p.stream = experts * MATS * p.N * p.Kd * 17 / 32 >= (128ll << 20);
+    if (p.cap <= 16ll * p.e_local) return launch_wide<MATS, 1, 2 / MATS, 4>(p, s);
+    if (p.cap <= 24ll * p.e_local) return launch_wide<MATS, 2, 1, 8>(p, s);
     // several row tiles an expert: 256 columns a workgroup, so that the rows are read half as often (512
-    // tokens: gate/up 173 against 175 us, down 106 against 119; 2048 tokens: 415 against 435 and 255 against 318)
-    return launch_wide<MATS, 2, 2, 8, false>(p, s);
+    // tokens: gate/up 170 against 176 us, down 106 against 117; 2048 tokens: 419 against 443 and 257 against 321)
+    return launch_wide<MATS, 2, 2, 8>(p, s);
 }
 
 // out[t] = bf16(sum over k ascending of gate[t,k] * y[pos[t,k]]) from fp32 rows: moe_combine without the rounding

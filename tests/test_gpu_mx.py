@@ -406,10 +406,11 @@ def test_gemm4_against_float64(counts, H, F):
     assert_equal("without y", bits(_lib.moe_grouped_gemm4_combine(*args)), bits(out))
 
 
-@pytest.mark.parametrize("rows", [3, 9, 20, 40])
+@pytest.mark.parametrize("rows", [3, 9, 20, 28, 40])
 def test_gemm4_large_matrices(rows):
-    """Matrices past half the last-level cache (the non-temporal loads) at every row tile: 40 experts of about
-    `rows` rows, one of them with three times as many and one with none, against float64 on the GPU."""
+    """Matrices past half the last-level cache (non-temporal loads for the experts of one row tile) at every row
+    tile: 40 experts of about `rows` rows, one of them with three times as many and one with none, against float64 on
+    the GPU."""
     E, Kd, N = 40, 4096, 2112
     rng = np.random.default_rng(rows)
     n = rng.integers(max(rows - 3, 1), rows + 2, E)
