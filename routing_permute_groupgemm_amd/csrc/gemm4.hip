@@ -437,9 +437,14 @@ static int launch_wide(const Gemm4Params& p, hipStream_t s) {
 //     (3): 36.8 against 34.4.  Down, one token (2): 7.4 against 8.0; two (4): 11.9
 //     against 10.7.  Two column tiles a workgroup once those make two workgroups a
 //     CU (gate/up of two tokens 19.9 against 22.9 us, of one 12.8 against 11.7).
-//   wide: row tiles of 16, or of 32 when there are more than 16 rows an expert
-//     (gate/up of 512 tokens, 128 experts: 173 against 202 us; 64 rows took 182 to 218;
-//     23 tokens, one or two rows an expert: 30 with 16 rows, 32 with 32).
+//   wide, rows: tiles of 16 up to two rows an expert, of 32 beyond.  128 experts, gate/up
+//     and down: 23 tokens 30 + 16 us with 16 rows, 33 + 18 with 32; 96 tokens (6 rows)
+//     133 + 74 against 128 + 73; 256 tokens (16) 165 + 97 against 147 + 83; 64 rows were
+//     slower at 512 tokens (182 to 218 us for gate/up).
+//   wide, columns of 32-row tiles: 256 a workgroup, which reads the rows half as often,
+//     once that leaves 4 workgroups a CU, else 128.  512 tokens: gate/up 170 against 183
+//     us, down 106 against 118; 64 tokens on 8 experts of 4096 columns (0.75): 52 against
+//     44; 256 tokens on 128 experts of 768 columns (2.3): 45 against 42.
 //   non-temporal weights (stream): when the packed matrices that the rows can touch
 //     fill half the last-level cache (128 MB) or more, so that they are not there the
 //     next time, for the experts whose rows fit one tile (gemm4_wide).
@@ -459,11 +464,10 @@ static int launch4_rows(Gemm4Params p, hipStream_t s) {
     }
     const int64_t experts = std::min<int64_t>(p.cap, p.e_local);
     p.stream = experts * MATS * p.N * p.Kd * 17 / 32 >= (128ll << 20);
-    if (p.cap <= 16ll * p.e_local) return launch_wide<MATS, 1, 2 / MATS, 4>(p, s);
-    if (p.cap <= 24ll * p.e_local) return launch_wide<MATS, 2, 1, 8>(p, s);
-    // several row tiles an expert: 256 columns a workgroup, so that the rows are read half as often (512
-    // tokens: gate/up 170 against 176 us, down 106 against 117; 2048 tokens: 419 against 443 and 257 against 321)
-    return launch_wide<MATS, 2, 2, 8>(p, s);
+    if (p.cap <= 2ll * p.e_local) return launch_wide<MATS, 1, 2 / MATS, 4>(p, s);
+    const int64_t wide = std::min<int64_t>(p.cap, p.cap / 32 + p.e_local) * ((p.N + 255) / 256);
+    if (wide >= 4 * cus) return launch_wide<MATS, 2, 2, 8>(p, s);
+    return launch_wide<MATS, 2, 1, 8>(p, s);
 }
 
 // out[t] = bf16(sum over k ascending of gate[t,k] * y[pos[t,k]]) from fp32 rows: moe_combine without the rounding

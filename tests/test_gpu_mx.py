@@ -406,15 +406,18 @@ def test_gemm4_against_float64(counts, H, F):
     assert_equal("without y", bits(_lib.moe_grouped_gemm4_combine(*args)), bits(out))
 
 
-@pytest.mark.parametrize("rows", [3, 9, 20, 28, 40])
-def test_gemm4_large_matrices(rows):
+@pytest.mark.parametrize("rows,Kd,N", [(1, 4096, 2112), (3, 4096, 2112), (9, 4096, 2112), (20, 4096, 2112),
+                                       (28, 4096, 2112), (40, 4096, 2112), (9, 1024, 6464), (40, 1024, 6464),
+                                       (5, 192, 6464), (20, 192, 6464)])
+def test_gemm4_large_matrices(rows, Kd, N):
     """Matrices past half the last-level cache (non-temporal loads for the experts of one row tile) at every row
-    tile: 40 experts of about `rows` rows, one of them with three times as many and one with none, against float64 on
+    tile, and many columns (256 a workgroup, the last of them partly empty), of small matrices too: 40 experts of
+    about `rows` rows, one of them with three times as many (18 for one row) and one with none, against float64 on
     the GPU."""
-    E, Kd, N = 40, 4096, 2112
+    E = 40
     rng = np.random.default_rng(rows)
     n = rng.integers(max(rows - 3, 1), rows + 2, E)
-    n[7], n[11] = 3 * rows, 0
+    n[7], n[11] = 3 * rows if rows > 1 else 18, 0
     off = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
     R = int(off[-1])
     gen = torch.Generator(device="cuda")
