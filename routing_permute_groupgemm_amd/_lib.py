@@ -103,6 +103,20 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _empty(shape, dtype, dev, stream, result=True):
+    """A new buffer for kernels on this stream (None: the current one).  It comes from that stream's memory: work
+    queued earlier on what the memory held, and later allocations once a workspace is dropped at the return, are
+    ordered with the kernels.  A result may be read on the current stream, which waits for the other first, so the
+    allocator is told of that stream: what is dropped there is not handed out while it is still being read."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if result:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def _device(stream, t):
     """The current device, which the stream (None: its current one) must belong to; t: a first argument, refused
     here if it is on the host (there may be no device then)."""
@@ -572,10 +586,10 @@ def _offsets(offsets, EL, dev):
         raise MoeError(f"offsets: expected {EL + 1} entries, got {offsets.numel()}")
 
 
-def _out(t, shape, dtype, name, dev, rows=None):
+def _out(t, shape, dtype, name, dev, stream, rows=None):
     """The caller's buffer (checked: at least `rows` rows, or exactly `shape`) or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return _empty(shape, dtype, dev, stream)
     _arg(t, dtype, name, dev)
     if rows is None:
         _shape(t, shape, name)
@@ -593,8 +607,8 @@ def moe_pack8(x, q=None, scale=None, offsets=None, stream=None):
         raise MoeError(f"x: expected [rows, a multiple of 64], got {tuple(x.shape)}")
     rows, cols = x.shape
     EL = _routed(offsets, dev)
-    q = _out(q, (rows, cols), torch.int8, "q", dev, rows)
-    scale = _out(scale, (rows, cols // 32), torch.uint8, "scale", dev, rows)
+    q = _out(q, (rows, cols), torch.int8, "q", dev, stream, rows)
+    scale = _out(scale, (rows, cols // 32), torch.uint8, "scale", dev, stream, rows)
     _check(load().moe_pack8(_ptr(x), rows, cols, _ptr(offsets), EL, _ptr(q), _ptr(scale), _handle(stream, dev)))
     return q, scale
 
@@ -609,12 +623,12 @@ def moe_unpack8(q, scale, x=None, offsets=None, stream=None):
     rows, cols = q.shape
     EL = _routed(offsets, dev)
     _rows(scale, rows, cols // 32, "scale")
-    x = _out(x, (rows, cols), torch.bfloat16, "x", dev, rows)
+    x = _out(x, (rows, cols), torch.bfloat16, "x", dev, stream, rows)
     _check(load().moe_unpack8(_ptr(q), _ptr(scale), rows, cols, _ptr(offsets), EL, _ptr(x), _handle(stream, dev)))
     return x
 
 
-def _save8_args(x, w_gate, w_up, offsets, cap_rows, h, ab8, ab8_scale, dev):
+def _save8_args(x, w_gate, w_up, offsets, cap_rows, h, ab8, ab8_scale, dev, stream):
     """Checks common to the two forms -> (EL, H, F, h, ab8, ab8_scale)."""
     for t, name in ((x, "x"), (w_gate, "w_gate"), (w_up, "w_up")):
         _arg(t, torch.bfloat16, name, dev)
@@ -624,9 +638,9 @@ def _save8_args(x, w_gate, w_up, offsets, cap_rows, h, ab8, ab8_scale, dev):
     _shape(w_up, (EL, H, F), "w_up")
     _offsets(offsets, EL, dev)
     n = max(cap_rows, 0)
-    h = _out(h, (n, F), torch.bfloat16, "h", dev, n)
-    ab8 = _out(ab8, (n, 2 * F), torch.int8, "ab8", dev, n)
-    ab8_scale = _out(ab8_scale, (n, 2 * F // 32), torch.uint8, "ab8_scale", dev, n)
+    h = _out(h, (n, F), torch.bfloat16, "h", dev, stream, n)
+    ab8 = _out(ab8, (n, 2 * F), torch.int8, "ab8", dev, stream, n)
+    ab8_scale = _out(ab8_scale, (n, 2 * F // 32), torch.uint8, "ab8_scale", dev, stream, n)
     return EL, H, F, h, ab8, ab8_scale
 
 
@@ -634,7 +648,8 @@ def moe_grouped_gemm_swiglu_save8(x_perm, w_gate, w_up, offsets, cap_rows, h=Non
                                   stream=None):
     """moe_grouped_gemm_swiglu with (a, b) saved in 8-bit blocks -> (h, ab8, ab8_scale)."""
     dev = _device(stream, x_perm)
-    EL, H, F, h, ab8, ab8_scale = _save8_args(x_perm, w_gate, w_up, offsets, cap_rows, h, ab8, ab8_scale, dev)
+    EL, H, F, h, ab8, ab8_scale = _save8_args(x_perm, w_gate, w_up, offsets, cap_rows, h, ab8, ab8_scale, dev,
+                                              stream)
     _rows(x_perm, cap_rows, H, "x_perm")
     _check(load().moe_grouped_gemm_swiglu_save8(_ptr(x_perm), _ptr(w_gate), _ptr(w_up), _ptr(offsets), EL, H, F,
                                                 cap_rows, _ptr(h), _ptr(ab8), _ptr(ab8_scale), _handle(stream, dev)))
@@ -645,7 +660,7 @@ def moe_grouped_gemm_swiglu_gather_save8(x, src, K, w_gate, w_up, offsets, cap_r
                                          ab8_scale=None, stream=None):
     """The same, reading row r of the expert-grouped order from x[src[r] // K] (no x_perm)."""
     dev = _device(stream, x)
-    EL, H, F, h, ab8, ab8_scale = _save8_args(x, w_gate, w_up, offsets, cap_rows, h, ab8, ab8_scale, dev)
+    EL, H, F, h, ab8, ab8_scale = _save8_args(x, w_gate, w_up, offsets, cap_rows, h, ab8, ab8_scale, dev, stream)
     _rows(x, 0, H, "x")
     _arg(src, torch.int32, "src", dev)
     if src.numel() < cap_rows:
@@ -672,8 +687,8 @@ def moe_grouped_gemm_swiglu_bwd8(dy_perm, w_down, offsets, cap_rows, ab8, ab8_sc
     _arg(ab8_scale, torch.uint8, "ab8_scale", dev)
     _rows(ab8_scale, cap_rows, 2 * F // 32, "ab8_scale")
     n = max(cap_rows, 0)
-    dab = _out(dab, (n, 2 * F), torch.bfloat16, "dab", dev, n)
-    h = _out(h, (n, F), torch.bfloat16, "h", dev, n) if want_h else None
+    dab = _out(dab, (n, 2 * F), torch.bfloat16, "dab", dev, stream, n)
+    h = _out(h, (n, F), torch.bfloat16, "h", dev, stream, n) if want_h else None
     _check(load().moe_grouped_gemm_swiglu_bwd8(_ptr(dy_perm), _ptr(w_down), _ptr(offsets), EL, H, F, cap_rows,
                                                _ptr(ab8), _ptr(ab8_scale), _ptr(dab), _ptr(h), _handle(stream, dev)))
     return dab, h
@@ -708,8 +723,8 @@ def moe_pack4(w, q4=None, s4=None, stream=None):
         raise MoeError(f"w: expected [E, Kd, N] with Kd and N multiples of 64, got {tuple(w.shape)}")
     E, Kd, N = w.shape
     q_shape, s_shape = pack4_shapes(E, Kd, N)
-    q4 = _out(q4, q_shape, torch.uint8, "q4", dev)
-    s4 = _out(s4, s_shape, torch.uint8, "s4", dev)
+    q4 = _out(q4, q_shape, torch.uint8, "q4", dev, stream)
+    s4 = _out(s4, s_shape, torch.uint8, "s4", dev, stream)
     _check(load().moe_pack4(_ptr(w), E, Kd, N, _ptr(q4), _ptr(s4), _handle(stream, dev)))
     return q4, s4
 
@@ -718,7 +733,7 @@ def moe_unpack4(q4, s4, Kd, w=None, stream=None):
     """The bf16 weights [E, Kd, N] that (q4, s4) stand for."""
     dev = _device(stream, q4)
     q4, s4, E, N = _weights4((q4, s4), Kd, "w", dev)
-    w = _out(w, (E, Kd, N), torch.bfloat16, "w", dev)
+    w = _out(w, (E, Kd, N), torch.bfloat16, "w", dev, stream)
     _check(load().moe_unpack4(_ptr(q4), _ptr(s4), E, Kd, N, _ptr(w), _handle(stream, dev)))
     return w
 
@@ -741,7 +756,7 @@ def moe_grouped_gemm4_swiglu(x, src, K, gate, up, offsets, cap_rows, h=None, str
         if src.numel() < cap_rows:
             raise MoeError(f"src: expected at least {cap_rows} entries, got {src.numel()}")
     n = max(cap_rows, 0)
-    h = _out(h, (n, F), torch.bfloat16, "h", dev, n)
+    h = _out(h, (n, F), torch.bfloat16, "h", dev, stream, n)
     _check(load().moe_grouped_gemm4_swiglu(_ptr(x), T, _ptr(src), int(K or 0), _ptr(gq), _ptr(gs), _ptr(uq),
                                            _ptr(us), _ptr(offsets), EL, H, F, cap_rows, _ptr(h),
                                            _handle(stream, dev)))
@@ -758,7 +773,7 @@ def moe_grouped_gemm4(a, w, offsets, cap_rows, c=None, stream=None):
     q4, s4, EL, N = _weights4(w, Kd, "w", dev)
     _offsets(offsets, EL, dev)
     n = max(cap_rows, 0)
-    c = _out(c, (n, N), torch.bfloat16, "c", dev, n)
+    c = _out(c, (n, N), torch.bfloat16, "c", dev, stream, n)
     _check(load().moe_grouped_gemm4(_ptr(a), _ptr(q4), _ptr(s4), _ptr(offsets), EL, Kd, N, cap_rows, _ptr(c),
                                     _handle(stream, dev)))
     return c
@@ -786,12 +801,12 @@ def moe_grouped_gemm4_combine(a, w, offsets, cap_rows, pos, gates, y=None, out=N
     if y is not None:
         _arg(y, torch.bfloat16, "y", dev)
         _rows(y, cap_rows, N, "y")
-    out = _out(out, (T, N), torch.bfloat16, "out", dev)
+    out = _out(out, (T, N), torch.bfloat16, "out", dev, stream)
     if ws is not None:
         _arg(ws, torch.uint8, "ws", dev)
     need = 4 * max(cap_rows, 0) * N  # as the library's own size, without a call
     if ws is None or ws.numel() < need:
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=a.device)
+        ws = _empty(max(need, 256), torch.uint8, dev, stream, result=False)
     _check(load().moe_grouped_gemm4_combine(_ptr(a), _ptr(q4), _ptr(s4), _ptr(offsets), EL, Kd, N, cap_rows,
                                             _ptr(pos), _ptr(gates), T, K, _ptr(y), _ptr(out), _ptr(ws), ws.numel(),
                                             _handle(stream, dev)))
