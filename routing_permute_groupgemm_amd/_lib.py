@@ -164,9 +164,9 @@ def moe_route(logits, K, topk_idx=None, gates=None, stream=None):
     _need(logits, torch.float32, "logits")
     T, E = logits.shape
     if topk_idx is None:
-        topk_idx = torch.empty((T, K), dtype=torch.int32, device=logits.device)
+        topk_idx = _empty((T, K), torch.int32, logits.device, stream)
     if gates is None:
-        gates = torch.empty((T, K), dtype=torch.float32, device=logits.device)
+        gates = _empty((T, K), torch.float32, logits.device, stream)
     _need(topk_idx, torch.int32, "topk_idx")
     _need(gates, torch.float32, "gates")
     _shape(topk_idx, (T, K), "topk_idx")
@@ -181,7 +181,7 @@ def moe_route_backward(topk_idx, gates, dgates, E, dlogits=None, stream=None):
     _need(dgates, torch.float32, "dgates")
     T, K = topk_idx.shape
     if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=torch.float32, device=gates.device)
+        dlogits = _empty((T, E), torch.float32, gates.device, stream)
     _need(dlogits, torch.float32, "dlogits")
     _shape(gates, (T, K), "gates")
     _shape(dgates, (T, K), "dgates")
@@ -208,27 +208,27 @@ def moe_permute(topk_idx, e_begin, e_local, x, cap_rows, out=None, ws=None, stre
     o = out or {}
     counts = o.get("counts")
     if counts is None:
-        counts = torch.empty(max(e_local, 1), dtype=torch.int32, device=dev)
+        counts = _empty(max(e_local, 1), torch.int32, dev, stream)
     offsets = o.get("offsets")
     if offsets is None:
-        offsets = torch.empty(e_local + 1, dtype=torch.int32, device=dev)
+        offsets = _empty(e_local + 1, torch.int32, dev, stream)
     pos = o.get("pos")
     if pos is None:
-        pos = torch.empty((T, K), dtype=torch.int32, device=dev)
+        pos = _empty((T, K), torch.int32, dev, stream)
     src = o.get("src")
     if src is None:
-        src = torch.empty(max(cap_rows, 1), dtype=torch.int32, device=dev)
+        src = _empty(max(cap_rows, 1), torch.int32, dev, stream)
     x_perm = o.get("x_perm")
     if x_perm is None and copy_rows:
-        x_perm = torch.empty((max(cap_rows, 1), H), dtype=torch.bfloat16, device=dev)
+        x_perm = _empty((max(cap_rows, 1), H), torch.bfloat16, dev, stream)
     if not copy_rows:
         x_perm = None
     status = o.get("status")
     if status is None:
-        status = torch.empty(4, dtype=torch.int32, device=dev)
+        status = _empty(4, torch.int32, dev, stream)
     need = moe_permute_workspace_size(T, K, e_local)
     if ws is None or ws.numel() < need:
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        ws = _empty(max(need, 256), torch.uint8, dev, stream)
     for t, name, dt in ((counts, "counts", torch.int32), (offsets, "offsets", torch.int32), (pos, "pos", torch.int32),
                         (src, "src", torch.int32), (status, "status", torch.int32)):
         _need(t, dt, name)
@@ -299,7 +299,7 @@ def moe_gather_gate_grad(d_out, pos, gates, y, dy_perm, dgates=None, stream=None
     _need(dy_perm, torch.bfloat16, "dy_perm")
     T, K = pos.shape
     if dgates is None:
-        dgates = torch.empty((T, K), dtype=torch.float32, device=d_out.device)
+        dgates = _empty((T, K), torch.float32, d_out.device, stream)
     _need(dgates, torch.float32, "dgates")
     H = d_out.shape[1]
     _shape(d_out, (T, H), "d_out")
@@ -332,7 +332,7 @@ def moe_grouped_gemm_swiglu(x_perm, w_gate, w_up, offsets, cap_rows, h=None, ab_
     _need(offsets, torch.int32, "offsets")
     EL, H, F = w_gate.shape
     if h is None:
-        h = torch.empty((x_perm.shape[0], F), dtype=torch.bfloat16, device=x_perm.device)
+        h = _empty((x_perm.shape[0], F), torch.bfloat16, x_perm.device, stream)
     _gate_up_checks(w_gate, w_up, offsets, cap_rows, h, ab_save)
     _rows(x_perm, cap_rows, H, "x_perm")
     _check(load().moe_grouped_gemm_swiglu(_ptr(x_perm), _ptr(w_gate), _ptr(w_up), _ptr(offsets), EL, H, F,
@@ -352,7 +352,7 @@ def moe_grouped_gemm_swiglu_gather(x, src, K, w_gate, w_up, offsets, cap_rows, h
     EL, H, F = w_gate.shape
     T = x.shape[0]
     if h is None:
-        h = torch.empty((max(cap_rows, 1), F), dtype=torch.bfloat16, device=x.device)
+        h = _empty((max(cap_rows, 1), F), torch.bfloat16, x.device, stream)
     _gate_up_checks(w_gate, w_up, offsets, cap_rows, h, ab_save)
     _shape(x, (T, H), "x")
     if src.numel() < cap_rows:
@@ -400,7 +400,7 @@ def moe_combine(y, pos, gates, out=None, stream=None):
     T, K = pos.shape
     H = y.shape[1]
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
+        out = _empty((T, H), torch.bfloat16, y.device, stream)
     _need(out, torch.bfloat16, "out")
     _shape(out, (T, H), "out")
     if gates is not None:
@@ -415,7 +415,7 @@ def moe_wgrad(a, lda, b, ldb, offsets, e_local, M, N, cap_rows, dw=None, a_col0=
     _need(b, torch.bfloat16, "b")
     _need(offsets, torch.int32, "offsets")
     if dw is None:
-        dw = torch.empty((e_local, M, N), dtype=torch.float32, device=a.device)
+        dw = _empty((e_local, M, N), torch.float32, a.device, stream)
     _need(dw, torch.float32, "dw")
     _shape(dw, (e_local, M, N), "dw")
     if offsets.numel() < e_local + 1:
@@ -447,7 +447,7 @@ def moe_wgrad_gate_up(x_perm, dab, offsets, e_local, cap_rows, dw_gate=None, dw_
     out = []
     for t, name in ((dw_gate, "dw_gate"), (dw_up, "dw_up")):
         if t is None:
-            t = torch.empty((e_local, H, F), dtype=torch.float32, device=x_perm.device)
+            t = _empty((e_local, H, F), torch.float32, x_perm.device, stream)
         _need(t, torch.float32, name)
         _shape(t, (e_local, H, F), name)
         out.append(t)
@@ -476,7 +476,7 @@ def moe_wgrad_gate_up_gather(x, src, K, dab, offsets, e_local, cap_rows, dw_gate
     out = []
     for t, name in ((dw_gate, "dw_gate"), (dw_up, "dw_up")):
         if t is None:
-            t = torch.empty((e_local, H, F), dtype=torch.float32, device=x.device)
+            t = _empty((e_local, H, F), torch.float32, x.device, stream)
         _need(t, torch.float32, name)
         _shape(t, (e_local, H, F), name)
         out.append(t)
@@ -497,7 +497,7 @@ def moe_wgrad_split(a, lda, b, ldb, offsets, e_local, M, N, cap_rows, splits, dw
     _need(b, torch.bfloat16, "b")
     _need(offsets, torch.int32, "offsets")
     if dw is None:
-        dw = torch.empty((e_local, M, N), dtype=torch.float32, device=a.device)
+        dw = _empty((e_local, M, N), torch.float32, a.device, stream)
     _need(dw, torch.float32, "dw")
     _shape(dw, (e_local, M, N), "dw")
     if offsets.numel() < e_local + 1:
@@ -507,7 +507,7 @@ def moe_wgrad_split(a, lda, b, ldb, offsets, e_local, M, N, cap_rows, splits, dw
             raise MoeError(f"{name}: too small for {cap_rows} rows at stride {ld} from column {c0}")
     need = moe_wgrad_split_workspace_size(e_local, M, N, splits)
     if ws is None or ws.numel() < need:
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=a.device)
+        ws = _empty(max(need, 256), torch.uint8, a.device, stream, result=False)
     pa = a.data_ptr() + 2 * a_col0
     pb = b.data_ptr() + 2 * b_col0
     _check(load().moe_wgrad_split(pa, lda, pb, ldb, _ptr(offsets), e_local, M, N, cap_rows, splits, _ptr(dw),
@@ -519,10 +519,10 @@ def moe_router_workspace_size(T, H, E) -> int:
     return int(load().moe_router_workspace_size(T, H, E))
 
 
-def _router_ws(T, H, E, ws, dev):
+def _router_ws(T, H, E, ws, dev, stream):
     need = moe_router_workspace_size(T, H, E)
     if ws is None or ws.numel() < need:
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        ws = _empty(max(need, 256), torch.uint8, dev, stream, result=False)
     return ws
 
 
@@ -535,13 +535,13 @@ def moe_router_logits(x, w_r, bias=None, logits=None, ws=None, stream=None):
     T, H = x.shape
     E = w_r.shape[1]
     if logits is None:
-        logits = torch.empty((T, E), dtype=torch.float32, device=x.device)
+        logits = _empty((T, E), torch.float32, x.device, stream)
     _shape(w_r, (H, E), "w_r")
     if bias is not None:
         _shape(bias, (E,), "bias")
     _need(logits, torch.float32, "logits")
     _shape(logits, (T, E), "logits")
-    ws = _router_ws(T, H, E, ws, x.device)
+    ws = _router_ws(T, H, E, ws, x.device, stream)
     _check(load().moe_router_logits(_ptr(x), T, H, _ptr(w_r), E, _ptr(bias), _ptr(logits), _ptr(ws), ws.numel(),
                                     _stream(stream)))
     return logits
@@ -555,16 +555,16 @@ def moe_router_backward(x, w_r, dlogits, dx=None, dw_r=None, ws=None, stream=Non
     T, H = x.shape
     E = w_r.shape[1]
     if dx is None:
-        dx = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        dx = _empty((T, H), torch.bfloat16, x.device, stream)
     if dw_r is None:
-        dw_r = torch.empty((H, E), dtype=torch.float32, device=x.device)
+        dw_r = _empty((H, E), torch.float32, x.device, stream)
     _shape(w_r, (H, E), "w_r")
     _shape(dlogits, (T, E), "dlogits")
     _need(dx, torch.bfloat16, "dx")
     _shape(dx, (T, H), "dx")
     _need(dw_r, torch.float32, "dw_r")
     _shape(dw_r, (H, E), "dw_r")
-    ws = _router_ws(T, H, E, ws, x.device)
+    ws = _router_ws(T, H, E, ws, x.device, stream)
     _check(load().moe_router_backward(_ptr(x), T, H, _ptr(w_r), E, _ptr(dlogits), _ptr(dx), _ptr(dw_r), _ptr(ws),
                                       ws.numel(), _stream(stream)))
     return dx, dw_r
@@ -821,7 +821,7 @@ def moe_probe_mfma(operands, iters, out=None, stream=None):
         raise MoeError(f"operands: expected shape (4*blocks, 8, 64, 8), got {tuple(operands.shape)}")
     waves = operands.shape[0]
     if out is None:
-        out = torch.empty((waves, 64), dtype=torch.float32, device=operands.device)
+        out = _empty((waves, 64), torch.float32, operands.device, stream)
     _need(out, torch.float32, "out")
     _shape(out, (waves, 64), "out")
     _check(load().moe_probe_mfma(_ptr(operands), waves // 4, iters, _ptr(out), _stream(stream)))
@@ -836,7 +836,7 @@ def moe_probe_mfma16(operands, iters, out=None, stream=None):
         raise MoeError(f"operands: expected shape (4*blocks, 16, 64, 8), got {tuple(operands.shape)}")
     waves = operands.shape[0]
     if out is None:
-        out = torch.empty((waves, 64), dtype=torch.float32, device=operands.device)
+        out = _empty((waves, 64), torch.float32, operands.device, stream)
     _need(out, torch.float32, "out")
     _shape(out, (waves, 64), "out")
     _check(load().moe_probe_mfma16(_ptr(operands), waves // 4, iters, _ptr(out), _stream(stream)))

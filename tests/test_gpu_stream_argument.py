@@ -71,3 +71,27 @@ def test_a_result_dropped_while_the_current_stream_reads_it(data):
         again = [torch.full((T, H), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
     torch.cuda.synchronize()
     assert torch.equal(copy, data["want"]) and all((t == 7.0).all() for t in again)
+
+
+def test_layer_calls_with_a_workspace_of_their_own(data):
+    """The split weight gradient and the router's backward on two streams at once, without buffers."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(61)
+    a, b = normal(gen, ROWS, H), normal(gen, ROWS, F)
+    x, w_r = normal(gen, T, H), normal(gen, H, 64, std=0.05)
+    dlogits = torch.randn((T, 64), generator=gen, device="cuda")
+
+    def calls(stream=None):
+        dw = _lib.moe_wgrad_split(a, H, b, F, data["offsets"], E, H, F, ROWS, 2, stream=stream)
+        return (dw, *_lib.moe_router_backward(x, w_r, dlogits, stream=stream))
+
+    want = calls()
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for _ in range(4):
+        for s in streams:
+            got.append(calls(s))
+            torch.full((E * 2 * H * F,), 7.0, device="cuda")
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(p, q) for p, q in zip(g, want))

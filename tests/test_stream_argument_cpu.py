@@ -112,3 +112,31 @@ def test_without_a_stream_the_current_one_allocates(traced, monkeypatch):
     monkeypatch.setattr(_lib, "_handle", lambda stream, dev: 0x52)
     _lib.moe_pack8(z(4, 64))
     assert set(traced.owner.values()) == {None} and not traced.recorded
+
+
+LAYER = {
+    "route": lambda s: _lib.moe_route(z(4, 8, dtype=F32), 2, stream=s),
+    "route_backward": lambda s: _lib.moe_route_backward(z(4, 2, dtype=I32), z(4, 2, dtype=F32), z(4, 2, dtype=F32), 8,
+                                                        stream=s),
+    "permute": lambda s: tuple(_lib.moe_permute(z(4, 2, dtype=I32), 0, 8, z(4, 64), 8, stream=s).values()),
+    "swiglu": lambda s: _lib.moe_grouped_gemm_swiglu(z(4, 64), z(2, 64, 64), z(2, 64, 64), OFF, 4, stream=s),
+    "swiglu_gather": lambda s: _lib.moe_grouped_gemm_swiglu_gather(z(4, 64), z(4, dtype=I32), 1, z(2, 64, 64),
+                                                                   z(2, 64, 64), OFF, 4, stream=s),
+    "combine": lambda s: _lib.moe_combine(z(4, 64), z(4, 1, dtype=I32), None, stream=s),
+    "gather_gate_grad": lambda s: _lib.moe_gather_gate_grad(z(4, 64), z(4, 1, dtype=I32), z(4, 1, dtype=F32),
+                                                            z(4, 64), z(4, 64), stream=s)[1],
+    "wgrad": lambda s: _lib.moe_wgrad(z(4, 64), 64, z(4, 64), 64, OFF, 2, 64, 64, 4, stream=s),
+    "wgrad_gate_up": lambda s: _lib.moe_wgrad_gate_up(z(4, 64), z(4, 128), OFF, 2, 4, stream=s),
+    "wgrad_gate_up_gather": lambda s: _lib.moe_wgrad_gate_up_gather(z(4, 64), z(4, dtype=I32), 1, z(4, 128), OFF, 2, 4,
+                                                                    stream=s),
+    "wgrad_split": lambda s: _lib.moe_wgrad_split(z(4, 64), 64, z(4, 64), 64, OFF, 2, 64, 64, 4, 2, stream=s),
+    "router_logits": lambda s: _lib.moe_router_logits(z(4, 64), z(64, 8), stream=s),
+    "router_backward": lambda s: _lib.moe_router_backward(z(4, 64), z(64, 8), z(4, 8, dtype=F32), stream=s),
+    "probe_mfma": lambda s: _lib.moe_probe_mfma(z(4, 8, 64, 8), 1, stream=s),
+    "probe_mfma16": lambda s: _lib.moe_probe_mfma16(z(4, 16, 64, 8), 1, stream=s),
+}
+
+
+@pytest.mark.parametrize("name", list(LAYER))
+def test_buffers_of_the_layer_calls(name, traced):
+    check(traced, LAYER[name])
