@@ -59,7 +59,11 @@ class MoeBuffers:
         if weights4:  # serving: the products read the tokens through src
             backward, zero_copy = False, True
         T, H, F, K, EL = shape.T, shape.H, shape.F, shape.K, shape.EL
-        cap = shape.cap if cap is None else cap
+        if cap is None:
+            # shape.cap is twice a share's expected rows, which a few tokens exceed now and then (one token on 32 of
+            # 256 experts, top 8: 1 step in 15).  A decode step keeps room for every pair that can be local instead;
+            # its rows are few
+            cap = T * min(K, EL) if weights4 else shape.cap
         capn = max(cap, 1)
         e = lambda *s, dt=torch.bfloat16: torch.empty(*s, dtype=dt, device=device)  # noqa: E731
         ws_bytes = max(_lib.moe_permute_workspace_size(T, K, EL), 256)
@@ -145,7 +149,8 @@ def pack_weights4(inp: dict) -> dict:
 
 def forward4(buf: MoeBuffers, inp: dict):
     """The forward of a decode step on 4-bit weights. inp: device tensors logits and x, and pack_weights4's
-    pairs; buffers allocated with weights4=True."""
+    pairs; buffers allocated with weights4=True, whose own capacity holds every local pair (with a smaller one
+    given, the pairs beyond it are dropped and buf.status says so, as in forward)."""
     s = buf.shape
     if not buf.weights4:
         raise _lib.MoeError("forward4: the buffers need weights4=True")
