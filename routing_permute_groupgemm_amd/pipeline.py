@@ -44,7 +44,7 @@ class MoeBuffers:
     # GroupGEMM and the gate/up weight gradient read x[src[r] // K]
     zero_copy: bool = False
     # 8-bit checkpoint: the forward saves (a, b) in 8-bit blocks instead of ab, and the backward recomputes
-    # h from them, so h is scratch that layers may share
+    # h from them, so h is scratch that layers may share (allocate's h)
     checkpoint8: bool = False
     # 4-bit weights (forward4): the experts' rows stay in fp32 in ws4, there is no y
     weights4: bool = False
@@ -54,7 +54,9 @@ class MoeBuffers:
 
     @classmethod
     def allocate(cls, shape: MoeShape, cap: int | None = None, device="cuda", backward=None, zero_copy=False,
-                 checkpoint8=False, weights4=False):
+                 checkpoint8=False, weights4=False, h: torch.Tensor | None = None):
+        """h: a buffer to use as buf.h, bf16 [at least cap, F], that layers run in turn on one stream may share:
+        with checkpoint8 or without a backward, where nothing is kept in h between two steps."""
         backward = shape.backward if backward is None else backward
         if weights4:  # serving: the products read the tokens through src
             backward, zero_copy = False, True
@@ -65,6 +67,13 @@ class MoeBuffers:
             # its rows are few
             cap = T * min(K, EL) if weights4 else shape.cap
         capn = max(cap, 1)
+        if h is not None:
+            if backward and not checkpoint8:
+                raise _lib.MoeError("h: the backward reads it unless checkpoint8 is set, so layers cannot share it")
+            if (h.dtype != torch.bfloat16 or not h.is_contiguous() or h.device.type != torch.device(device).type
+                    or h.dim() != 2 or h.shape[0] < cap or h.shape[1] != F):
+                raise _lib.MoeError(f"h: expected a contiguous bfloat16 tensor of at least {cap} rows of {F} columns on "
+                                    f"{device}, got {h.dtype} {tuple(h.shape)} on {h.device}")
         e = lambda *s, dt=torch.bfloat16: torch.empty(*s, dtype=dt, device=device)  # noqa: E731
         ws_bytes = max(_lib.moe_permute_workspace_size(T, K, EL), 256)
         b = cls(shape=shape, cap=cap,
@@ -72,7 +81,8 @@ class MoeBuffers:
                 counts=e(max(EL, 1), dt=torch.int32), offsets=e(EL + 1, dt=torch.int32),
                 pos=e((T, K), dt=torch.int32), src=e(capn, dt=torch.int32),
                 x_perm=None if zero_copy else e((capn, H)),
-                status=e(4, dt=torch.int32), ws=e(ws_bytes, dt=torch.uint8), h=e((capn, F)),
+                status=e(4, dt=torch.int32), ws=e(ws_bytes, dt=torch.uint8),
+                h=e((capn, F)) if h is None else h,
                 ab=e((capn, 2 * F)) if backward and not checkpoint8 else None,
                 y=None if weights4 else e((capn, H)), out=e((T, H)), zero_copy=zero_copy,
                 checkpoint8=checkpoint8 and backward, weights4=weights4)
@@ -164,7 +174,7 @@ def forward4(buf: MoeBuffers, inp: dict):
 
 def backward(buf: MoeBuffers, inp: dict):
     """inp additionally holds d_out (and x, read by the zero-copy weight gradient). Needs the forward's
-    ab_save, or its 8-bit (a, b), from which h is recomputed into buf.h."""
+    ab_save, or its 8-bit (a, b), from which h is recomputed into buf.h (whatever it holds by then)."""
     s = buf.shape
     H, F, EL, cap = s.H, s.F, s.EL, buf.cap
     _lib.moe_gather_gate_grad(inp["d_out"], buf.pos, buf.gates, buf.y, buf.dy_perm, buf.dgates)
