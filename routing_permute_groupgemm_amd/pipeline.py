@@ -57,6 +57,8 @@ class MoeBuffers:
                  checkpoint8=False, weights4=False, h: torch.Tensor | None = None):
         """h: a buffer to use as buf.h, bf16 [at least cap, F], that layers run in turn on one stream may share:
         with checkpoint8 or without a backward, where nothing is kept in h between two steps."""
+        if weights4 and (backward or checkpoint8):
+            raise _lib.MoeError("allocate: 4-bit weights are for the forward only, without backward or checkpoint8")
         backward = shape.backward if backward is None else backward
         if weights4:  # serving: the products read the tokens through src
             backward, zero_copy = False, True

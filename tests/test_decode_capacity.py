@@ -55,3 +55,13 @@ def test_decode_step_with_more_rows_than_twice_the_expected(T, seed, local):
             mag += g * (h.abs() @ w["w_down"][e].abs())
         # fp32 sums of 192 products and of 8 gated rows, and one rounding to bf16
         assert ((out[t].double() - want).abs() <= (192 + 16) * 2.0 ** -24 * mag + 2.0 ** -8 * want.abs() + 1e-37).all()
+
+
+def test_4bit_buffers_refuse_a_backward():
+    """An explicit backward or checkpoint was dropped without a word; a shape that has a backward may still serve."""
+    for kw in (dict(backward=True), dict(checkpoint8=True), dict(backward=True, checkpoint8=True)):
+        with pytest.raises(_lib.MoeError):
+            pipeline.MoeBuffers.allocate(SHARE.scaled(T=4), weights4=True, device="cpu", **kw)
+    for shape, backward in ((SHARE.scaled(T=4, backward=True), None), (SHARE.scaled(T=4), False)):
+        buf = pipeline.MoeBuffers.allocate(shape, weights4=True, device="cpu", backward=backward)
+        assert buf.dx is None and buf.ab8 is None and not buf.checkpoint8
