@@ -481,7 +481,7 @@ int moe_grouped_gemm4(const moe_bf16* a, const uint8_t* q4, const uint8_t* s4, c
  * to bf16 in between:
  *   out[t] = bf16(sum over k ascending with 0 <= pos[t,k] < cap_rows of gates[t,k] * (a[pos[t,k]] . w))
  * A token without such a pair gets +0.  y, if not NULL, gets the rows a[r] . w rounded
- * to bf16.
+ * to bf16 (with T = 0 too, where pos, gates and out are not used).
  *   pos int32 [T,K], gates fp32 [T,K];  y bf16 [cap_rows,N] or NULL;  out bf16 [T,N];
  *   ws: device workspace of at least moe_gemm4_combine_workspace_size(cap_rows, N)
  *   bytes (the fp32 rows), one for each of calls that may overlap.  T <= 262140;

@@ -591,8 +591,9 @@ extern "C" int moe_grouped_gemm4_combine(const moe_bf16* a, const uint8_t* q4, c
     if (rc != MOE_OK) return rc;
     if (T < 0 || K < 1 || K > 16 || (int64_t)T * K >= (1ll << 31)) return MOE_EINVAL;
     if (T > 4 * 65535) return MOE_EINVAL;
-    if (T == 0 || N == 0) return MOE_OK;
-    if (!pos || !gates || !out) return MOE_EINVAL;
+    // without tokens there is no sum, but the rows may still be asked for
+    if (N == 0 || (T == 0 && (nothing || !y))) return MOE_OK;
+    if (T > 0 && (!pos || !gates || !out)) return MOE_EINVAL;
     if (!nothing && (!a || !q4 || !s4)) return MOE_EINVAL;
     if (misaligned(a) || misaligned(q4) || misaligned(s4) || misaligned(offsets) || misaligned(pos) ||
         misaligned(gates) || misaligned(y) || misaligned(out) || misaligned(ws))
@@ -618,6 +619,7 @@ extern "C" int moe_grouped_gemm4_combine(const moe_bf16* a, const uint8_t* q4, c
         const int st = launch4_rows<1>(p, s);
         if (st != MOE_OK) return st;
     }
+    if (T == 0) return MOE_OK;
     // with no expert or no row here, every token's sum is empty: cap 0 takes no row
     combine32_kernel<<<dim3((N / 4 + 63) / 64, (T + 3) / 4), 256, 0, s>>>((const float*)ws, nothing ? 0 : cap_rows,
                                                                           pos, gates, T, K, N, out);
