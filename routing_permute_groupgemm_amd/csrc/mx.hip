@@ -164,8 +164,10 @@ __global__ __launch_bounds__(256) void unpack4_kernel(const u32x4* __restrict__ 
     }
 }
 
+// A workgroup for every 512 chunks, as far as a launch may have threads (below 2^32: 2^36 values, which the
+// loop then takes in several steps).
 static int grid8(int64_t chunks) {
-    return (int)std::min<int64_t>((chunks + 256 * kChunks - 1) / (256 * kChunks), 0x7fffffff);
+    return (int)std::min<int64_t>((chunks + 256 * kChunks - 1) / (256 * kChunks), (1 << 24) - 1);
 }
 
 static bool streams8(int64_t rows, int cols) { return rows * cols * 2 >= (64ll << 20); }

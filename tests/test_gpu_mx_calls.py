@@ -23,3 +23,53 @@ def test_combine_without_tokens_writes_the_rows(rows):
                                          torch.empty((0, 2), device="cuda"), y=y)
     assert out.shape == (0, 128)
     assert torch.equal(y[:rows], _lib.moe_grouped_gemm4(a, w, offsets, rows)) and (y[rows:] == 5.0).all()
+
+
+def test_pack8_of_a_buffer_past_2_36_values():
+    """2^24 rows of 4096 with three of them routed: a grid of as many workgroups as the buffer has chunks would
+    have 2^32 threads, which no launch may have."""
+    x = normal(3, 3, 4096)
+    offsets = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    want_q, want_s = _lib.moe_pack8(x)
+    q, s = torch.full((4, 4096), 55, dtype=torch.int8, device="cuda"), torch.full((4, 128), 9, dtype=torch.uint8,
+                                                                                  device="cuda")
+    v = torch.full((4, 4096), 5.0, dtype=torch.bfloat16, device="cuda")
+    lib, st = _lib.load(), torch.cuda.current_stream().cuda_stream
+    # only the routed rows are touched, so the buffers need hold no more
+    assert lib.moe_pack8(x.data_ptr(), 1 << 24, 4096, offsets.data_ptr(), 1, q.data_ptr(), s.data_ptr(), st) == 0
+    assert lib.moe_unpack8(q.data_ptr(), s.data_ptr(), 1 << 24, 4096, offsets.data_ptr(), 1, v.data_ptr(), st) == 0
+    assert torch.equal(q[:3], want_q) and torch.equal(s[:3], want_s)
+    assert torch.equal(v[:3], _lib.moe_unpack8(want_q, want_s))
+    assert (q[3] == 55).all() and (s[3] == 9).all() and (v[3] == 5.0).all()
+
+
+def test_pack8_of_2_36_values():
+    """The same sizes with every row there: the rows behind the first 2^36 - 4096 values are a workgroup's second
+    step, and are packed and unpacked like the others."""
+    torch.cuda.empty_cache()
+    rows, cols = (1 << 24) + 3, 4096
+    need = rows * cols * 3 + rows * cols // 32
+    if torch.cuda.mem_get_info()[0] < need + (12 << 30):
+        pytest.skip(f"needs {need >> 30} GiB of free memory")
+    x = torch.full((rows, cols), 1.0, dtype=torch.bfloat16, device="cuda")
+    probe = [0, 1, 1 << 23, (1 << 24) - 2, (1 << 24) - 1, 1 << 24, rows - 1]
+    want = normal(4, len(probe), cols)
+    x[probe] = want
+    wq, ws = _lib.moe_pack8(want)
+    print(f"[mx] pack8 of {rows} x {cols}", flush=True)
+    q, s = _lib.moe_pack8(x)
+    torch.cuda.synchronize()
+    assert torch.equal(q[probe], wq) and torch.equal(s[probe], ws)
+    x.fill_(3.0)
+    print("[mx] unpack8", flush=True)
+    _lib.moe_unpack8(q, s, x)
+    torch.cuda.synchronize()
+    assert torch.equal(x[probe], _lib.moe_unpack8(wq, ws))
+    x[probe], q[probe], s[probe] = 1.0, 64, 127  # 1.0 is 64 steps of 2^-6
+    for lo in range(0, rows, 1 << 20):
+        part = slice(lo, lo + (1 << 20))
+        for t, v in ((x, 1.0), (q, 64), (s, 127)):
+            a, b = torch.aminmax(t[part])
+            assert float(a) == float(b) == v, (lo, v)
+    del x, q, s
+    torch.cuda.empty_cache()
