@@ -467,7 +467,8 @@ int moe_unpack4(const uint8_t* q4, const uint8_t* s4, int E, int Kd, int N, moe_
  *   a bf16 [cap_rows,Kd];  q4, s4 packed from [e_local,Kd,N];  c bf16 [cap_rows,N].
  * A src value outside [0, T*K) reads a zero row.  Errors as
  * moe_grouped_gemm_swiglu_gather (x at most 0xF0000000 bytes, cap_rows <= T*K,
- * one expert's matrix below 2^30 values).
+ * one expert's matrix below 2^30 values), and MOE_EINVAL where a launch would
+ * need 2^32 threads: from about 2^36 values of h or c (cap_rows * F or N) on.
  */
 int moe_grouped_gemm4_swiglu(const moe_bf16* x, int T, const int32_t* src, int K, const uint8_t* gate_q4,
                              const uint8_t* gate_s4, const uint8_t* up_q4, const uint8_t* up_s4,

@@ -412,11 +412,15 @@ __global__ __launch_bounds__(64 * W) void gemm4_wide(Gemm4Params p) {
     else wide_tile<MATS, MT, NT, W, false>(p, xs, j, row0, rows, slab);
 }
 
+// Whether a launch may have this many workgroups of W waves: its threads stay below 2^32 (and the tile numbers
+// below 2^31).
+static bool too_many(int64_t grid, int W) { return grid * (64 * W) >= (1ll << 32); }
+
 template <int MATS, int NT, int W>
 static int launch_split(const Gemm4Params& p, hipStream_t s) {
     const int64_t tiles = std::min<int64_t>(p.cap, p.cap / 16 + p.e_local);
     const int64_t grid = (tiles * ((p.N / 16 + NT - 1) / NT) + 7) / 8 * 8;
-    if (grid >= (1ll << 31)) return MOE_EINVAL;
+    if (too_many(grid, W)) return MOE_EINVAL;
     gemm4_split<MATS, NT, W><<<(unsigned)grid, 64 * W, 0, s>>>(p);
     return moe_host::launch_status();
 }
@@ -425,7 +429,7 @@ template <int MATS, int MT, int NT, int W>
 static int launch_wide(const Gemm4Params& p, hipStream_t s) {
     const int64_t tiles = std::min<int64_t>(p.cap, p.cap / (16 * MT) + p.e_local);
     const int64_t grid = (tiles * ((p.N / 16 + NT * W - 1) / (NT * W)) + 7) / 8 * 8;
-    if (grid >= (1ll << 31)) return MOE_EINVAL;
+    if (too_many(grid, W)) return MOE_EINVAL;
     gemm4_wide<MATS, MT, NT, W><<<(unsigned)grid, 64 * W, 0, s>>>(p);
     return moe_host::launch_status();
 }

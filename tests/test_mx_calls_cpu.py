@@ -19,3 +19,15 @@ def test_combine_without_tokens_still_has_rows_to_write():
         assert combine(**none, y=FAKE, **{n: None}) == -1, n
     assert combine(**none, y=FAKE, ws=None) == -4
     assert combine(**none, y=FAKE, cap=0) == 0 and combine(**none, y=FAKE, el=0) == 0 and combine(**none, y=FAKE, N=0) == 0
+
+
+def test_gemm4_refuses_what_no_launch_can_hold():
+    """2^32 threads and more: 2^17 row tiles of 32 rows (and one per expert) x 64 slabs of 256 columns, eight waves
+    each; and 576 row tiles of 16 rows x 2^17 slabs of 128 columns, four waves each."""
+    lib = _lib.load()
+    up = lib.moe_grouped_gemm4_swiglu
+    assert up(FAKE, 1 << 22, FAKE, 1, FAKE, FAKE, FAKE, FAKE, FAKE, 4, 64, 1 << 14, 1 << 22, FAKE, None) == -1
+    down = lib.moe_grouped_gemm4
+    assert down(FAKE, FAKE, FAKE, FAKE, 4, 64, 1 << 14, 1 << 22, FAKE, None) == -1
+    assert down(FAKE, FAKE, FAKE, FAKE, 512, 64, (1 << 24) - 64, 1024, FAKE, None) == -1
+    assert combine(T=1 << 18, cap=1 << 22, N=1 << 14, wsb=1 << 40) == -1
