@@ -382,7 +382,8 @@ int moe_router_backward(const moe_bf16* x, int T, int H, const moe_bf16* w_r, in
  * largest magnitude:
  *   s = max(biased exponent of m, 7)
  *   q = clamp(rint(x * 2^(133-s)), -127, 127)       (nearest even)
- *   value = q * 2^(s-133), a bf16;  |value - x| <= 2^(s-134) <= m/128
+ *   value = q * 2^(s-133), a bf16;  |value - x| <= 2^(s-134), which is at most
+ *   m/128 for m >= 2^-120 and 2^-127 below (where it may be all of x)
  *   q int8 [rows, cols], scale uint8 [rows, cols/32].
  *
  * 4 bits, weights [E][Kd][N] (blocks along the contraction Kd):

@@ -6,11 +6,12 @@
 //   s = max(biased exponent of m, 7),  q = clamp(rint(x * 2^(133-s)), -127, 127),
 //   value = q * 2^(s-133).
 // m * 2^(133-s) is below 128 (at most 127.5 for a bf16 m, so the clamp costs
-// no more than the half step of the rounding), and |value - x| <= 2^(s-134) <=
-// m / 128.  The products with the powers of two are exact, and the value has at
-// most 7 significant bits, so it is a bf16.  s >= 7 keeps the step 2^(s-133) a
-// normal number.  A block with a NaN or an infinity gets s = 255 and q = 0
-// and stands for NaN.
+// no more than the half step of the rounding), and |value - x| <= 2^(s-134),
+// which is at most m / 128 while s is m's own exponent (m >= 2^-120).  The
+// products with the powers of two are exact, and the value has at most 7
+// significant bits, so it is a bf16.  s >= 7 keeps the step 2^(s-133) a normal
+// number; below it the error is up to 2^-127, which may be all of x.  A block
+// with a NaN or an infinity gets s = 255 and q = 0 and stands for NaN.
 //
 // 4 bits (weights, blocks along the contraction): s = max(biased exponent of m - 2, 2),
 // value = c * 2^(s-127) with c one of +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}, rounded to

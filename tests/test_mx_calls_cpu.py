@@ -1,5 +1,8 @@
 """Calls of the block-scaled operators at the edges of what moe.h allows; everything here is decided on the host."""
-from routing_permute_groupgemm_amd import _lib
+import mx_ref
+import numpy as np
+
+from routing_permute_groupgemm_amd import _lib, synth
 
 FAKE = 0x10000  # never dereferenced
 
@@ -31,3 +34,21 @@ def test_gemm4_refuses_what_no_launch_can_hold():
     assert down(FAKE, FAKE, FAKE, FAKE, 4, 64, 1 << 14, 1 << 22, FAKE, None) == -1
     assert down(FAKE, FAKE, FAKE, FAKE, 512, 64, (1 << 24) - 64, 1024, FAKE, None) == -1
     assert combine(T=1 << 18, cap=1 << 22, N=1 << 14, wsb=1 << 40) == -1
+
+
+def test_8bit_error_at_the_scale_floor():
+    """Below 2^-120 the scale stays 7: a value is off by at most half a step of 2^-126, which may be all of it, and
+    from 2^-120 on by at most 1/128 of the block's largest magnitude."""
+    exact = np.zeros((1, 64), np.uint16)
+    exact[0, :3] = 0x0040, 0x0080, 0x0001                 # 2^-127 alone rounds to even, to 0; 2^-126 is one step
+    q, s = mx_ref.pack8(exact)
+    assert s[0, 0] == 7 and q[0, :3].tolist() == [0, 1, 0]
+    assert abs(mx_ref.unpack8(q, s)[0, 0] - 2.0 ** -127) == 2.0 ** -127 > 2.0 ** -126 / 128
+    for std in (2.0 ** -118, 2.0 ** -121, 2.0 ** -125, 2.0 ** -130):
+        bits = synth.f32_to_bf16_bits((np.random.default_rng(1).standard_normal((64, 256)) * std).astype(np.float32))
+        q, s = mx_ref.pack8(bits)
+        x, v = mx_ref.f64(bits), mx_ref.unpack8(q, s)
+        m = np.repeat(np.abs(x).reshape(64, -1, 32).max(2), 32, axis=1)
+        bound = np.where(m >= 2.0 ** -120, m / 128, 2.0 ** -127)
+        assert (np.abs(v - x) <= bound).all()
+    assert (np.abs(v - x) > m / 128).any()                # the floor is reached
