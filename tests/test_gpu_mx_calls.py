@@ -73,3 +73,25 @@ def test_pack8_of_2_36_values():
             assert float(a) == float(b) == v, (lo, v)
     del x, q, s
     torch.cuda.empty_cache()
+
+
+def test_gemm4_bits_of_a_row_go_by_the_sizes_alone():
+    """Two rows an expert: their bits stay when the other experts' rows change, and under another capacity, which
+    takes another kernel with another order of the sum, they differ by the roundings of two fp32 sums at most."""
+    E, Kd, N = 16, 2048, 1024
+    a, w = normal(5, 2 * E, Kd), _lib.moe_pack4(normal(6, E, Kd, N, std=0.05))
+    offsets = torch.arange(0, 2 * E + 1, 2, dtype=torch.int32, device="cuda")
+    got = _lib.moe_grouped_gemm4(a, w, offsets, 2 * E)
+    other = a.clone()
+    other[:6], other[8:] = 100.0, float("nan")
+    assert torch.equal(_lib.moe_grouped_gemm4(other, w, offsets, 2 * E)[6:8], got[6:8])
+    # an expert's two rows alone, and all rows under the capacity of many more
+    alone = torch.tensor([0] * 4 + [2] * 13, dtype=torch.int32, device="cuda")
+    one = _lib.moe_grouped_gemm4(a[6:8], w, alone, 2)
+    cap = 40 * E
+    many = _lib.moe_grouped_gemm4(torch.cat((a, a.new_zeros((cap - 2 * E, Kd)))), w, offsets, cap)
+    dense = _lib.moe_unpack4(*w, Kd)
+    want = torch.stack([a[r].double() @ dense[r // 2].double() for r in range(2 * E)])
+    tol = torch.stack([Kd * 2.0 ** -24 * (a[r].double().abs() @ dense[r // 2].double().abs()) for r in range(2 * E)])
+    for c, rows in ((got, slice(0, 2 * E)), (one, slice(6, 8)), (many[:2 * E], slice(0, 2 * E))):
+        assert ((c.double() - want[rows]).abs() <= tol[rows] + 2.0 ** -8 * want[rows].abs() + 1e-37).all()
