@@ -210,7 +210,7 @@ template <int MATS>
 __device__ __forceinline__ void store4(const Gemm4Params& p, int64_t r, int n, f32x4 v, f32x4 u) {
     if (MATS == 2) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = v[i] * __builtin_amdgcn_rcpf(1.0f + __expf(-v[i])) * u[i];
+        for (int i = 0; i < 4; ++i) v[i] = silu_f(v[i]) * u[i];
     }
     if (p.c) *(u32x2*)(p.c + r * p.N + n) = u32x2{pack_bf2x(v[0], v[1]), pack_bf2x(v[2], v[3])};
     if (MATS == 1 && p.c32) *(f32x4*)(p.c32 + r * p.N + n) = v;

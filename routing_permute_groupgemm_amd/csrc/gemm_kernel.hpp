@@ -270,9 +270,6 @@ struct Lay {
     }
 };
 
-__device__ __forceinline__ float sigmoid_f(float a) { return __builtin_amdgcn_rcpf(1.0f + __expf(-a)); }
-__device__ __forceinline__ float silu_f(float a) { return a * sigmoid_f(a); }
-
 __device__ __forceinline__ int xcd_remap(int b, int G) { return (b & 7) * (G >> 3) + (b >> 3); }
 
 // The lane id (0..63) read from the hardware where it is needed: the asm can be

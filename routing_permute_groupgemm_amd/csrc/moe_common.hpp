@@ -45,6 +45,9 @@ __device__ __forceinline__ uint32_t pack_bf2x(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
+__device__ __forceinline__ float sigmoid_f(float a) { return __builtin_amdgcn_rcpf(1.0f + __expf(-a)); }
+__device__ __forceinline__ float silu_f(float a) { return a * sigmoid_f(a); }
+
 // Buffer resource for raw (unstructured) buffer loads: `bytes` bounds the
 // valid range; loads at or past it return zero (and write zero to LDS for
 // LDS-direct loads).
