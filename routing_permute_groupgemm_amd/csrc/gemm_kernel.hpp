@@ -1957,13 +1957,13 @@ static int launch(const GemmParams& p, hipStream_t s) {
 }
 
 // The 8-bit forms' small grids: whether tiles of bm rows x cols columns all fit
-// the chip at once, two per CU, going by the sizes (an expert has cap / e_local
-// rows on average).  Larger tiles would then leave most CUs idle, and a tile's
-// epilogue, one wave per SIMD, is as long as the tile is large.
-inline bool fits_chip(const GemmParams& p, int bm, int cols) {
+// the chip at once, two per CU (or per_cu), going by the sizes (an expert has
+// cap / e_local rows on average).  Larger tiles would then leave most CUs idle,
+// and a tile's epilogue, one wave per SIMD, is as long as the tile is large.
+inline bool fits_chip(const GemmParams& p, int bm, int cols, int per_cu = 2) {
     if (tile_config() != CFG_AUTO) return false;
     const int64_t avg = (p.cap + p.e_local - 1) / p.e_local;
-    return (avg + bm - 1) / bm * p.e_local * ((p.N + cols - 1) / cols) <= 2 * (int64_t)moe_host::num_cus();
+    return (avg + bm - 1) / bm * p.e_local * ((p.N + cols - 1) / cols) <= per_cu * (int64_t)moe_host::num_cus();
 }
 
 // Launchers of the instantiations, each compiled in one translation unit

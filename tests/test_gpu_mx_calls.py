@@ -95,3 +95,23 @@ def test_gemm4_bits_of_a_row_go_by_the_sizes_alone():
     tol = torch.stack([Kd * 2.0 ** -24 * (a[r].double().abs() @ dense[r // 2].double().abs()) for r in range(2 * E)])
     for c, rows in ((got, slice(0, 2 * E)), (one, slice(6, 8)), (many[:2 * E], slice(0, 2 * E))):
         assert ((c.double() - want[rows]).abs() <= tol[rows] + 2.0 ** -8 * want[rows].abs() + 1e-37).all()
+
+
+@pytest.mark.parametrize("H,E,rows,F", [(512, 8, 64, 2304), (576, 8, 64, 2304), (2048, 4, 250, 1024), (2112, 4, 120, 1024),
+                                        (2112, 4, 250, 2048), (3648, 7, 60, 1984), (4096, 6, 64, 2048),
+                                        (4160, 3, 64, 2048), (4160, 7, 130, 512)])
+def test_save8_on_both_sides_of_its_tile_rule(H, E, rows, F):
+    """More panels of weights than CUs and fewer, contractions at the rule's borders: h and the bytes are the bf16
+    call's, bit for bit, whichever tiles the sizes choose."""
+    x, w = normal(7, E * rows, H), [normal(8 + i, E, H, F, std=0.02) for i in range(2)]
+    offsets = torch.arange(0, E * rows + 1, rows, dtype=torch.int32, device="cuda")
+    offsets[1:-1] += 3  # uneven
+    n = E * rows
+    ab = torch.empty((n, 2 * F), dtype=torch.bfloat16, device="cuda")
+    h = _lib.moe_grouped_gemm_swiglu(x, w[0], w[1], offsets, n, ab_save=ab)
+    q, s = _lib.moe_pack8(ab)
+    src = torch.arange(n, dtype=torch.int32, device="cuda")
+    for got in (_lib.moe_grouped_gemm_swiglu_save8(x, w[0], w[1], offsets, n),
+                _lib.moe_grouped_gemm_swiglu_gather_save8(x, src, 1, w[0], w[1], offsets, n)):
+        for a, b in zip(got, (h, q, s)):
+            assert torch.equal(a, b)
