@@ -37,7 +37,10 @@ sys.path.insert(0, ROOT)
 HBM_PEAK_GBS = 8000.0        # MI355X HBM3E
 MFMA_BF16_PEAK_TFS = 2500.0  # MI355X dense bf16 MFMA
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic.json")
-GEMM_SRCS = os.path.join(ROOT, "routing_permute_groupgemm_amd", "csrc", "gemm*")
+CSRC = os.path.join(ROOT, "routing_permute_groupgemm_amd", "csrc")
+# what the GroupGEMM launches of a layer step are compiled from: their translation units and every header of theirs
+GEMM_SRCS = ("gemm_dgrad.hip", "gemm_gather.hip", "gemm_rows.hip", "gemm_swiglu.hip", "gemm_wgrad.hip",
+             "gemm_kernel.hpp", "moe_common.hpp", "mx.hpp")
 
 
 def parse():
@@ -173,13 +176,12 @@ def roofline(work, ms):
                 frac=round(ach / HBM_PEAK_GBS, 4))
 
 
-def src_hash():
-    """Hash of the GroupGEMM sources (kernel header and its translation units)."""
-    import glob
+def src_hash(csrc=CSRC):
+    """Hash of the sources that the counted GroupGEMM launches are compiled from."""
     h = hashlib.sha256()
-    for path in sorted(glob.glob(GEMM_SRCS)):
-        with open(path, "rb") as fh:
-            h.update(os.path.basename(path).encode() + b"\0" + fh.read())
+    for name in GEMM_SRCS:
+        with open(os.path.join(csrc, name), "rb") as fh:
+            h.update(name.encode() + b"\0" + fh.read())
     return h.hexdigest()[:16]
 
 
