@@ -464,7 +464,7 @@ int moe_unpack4(const uint8_t* q4, const uint8_t* s4, int E, int Kd, int N, moe_
  *   h[r] = bf16(silu(x_r . w_gate[j]) * (x_r . w_up[j])),   c[r] = bf16(a[r] . w[j])
  * with x_r = x[src[r] / K], or x[r] if src is NULL (x then has cap_rows rows in
  * expert order; T and K are not used).  fp32 sums in an order that the
- * sizes and the GPU's number of CUs decide (for a token or two the contraction
+ * sizes and the GPU's number of CUs decide (for few row tiles the contraction
  * is cut into four partial sums): calls of equal sizes give a row the same bits
  * whatever the other rows are, calls of another cap_rows or e_local may not.
  *   x bf16 [T,H];  gate, up packed from [e_local,H,F];  h bf16 [cap_rows,F];

@@ -20,8 +20,8 @@
 // Two kernels share this:
 //   gemm4_split: the waves of a workgroup take the contraction tiles of the
 //     same 16 rows x 16*NT columns in turn; their fp32 sums meet in LDS, added
-//     in wave order.  For one token or two, whose tiles are too few to give
-//     every SIMD a wave of its own columns.
+//     in wave order.  For a few tokens, whose tiles are too few to give every SIMD
+//     a wave of its own columns.
 //   gemm4_wide: every wave has its own 16*NT columns and runs the whole
 //     contraction; the rows, which the waves share, go through LDS.  Nothing is
 //     reduced across waves, and a row byte is read once per workgroup.
@@ -218,7 +218,7 @@ __device__ __forceinline__ void store4(const Gemm4Params& p, int64_t r, int n, f
 
 // 16 rows x 16*NT columns of a workgroup, the contraction tiles over its W waves.
 // Measured for one token (H = 4096, F = 1536, 8 experts): gate/up 11.7 us for
-// 53 MB of weights, down 7.4 us for 27 MB; gemm4_wide took 16.5 and 8.0.
+// 53 MB of weights, down 7.4 us for 27 MB.
 template <int MATS, int NT, int W>
 __global__ __launch_bounds__(64 * W) void gemm4_split(Gemm4Params p) {
     constexpr int ACC = MATS * NT;
@@ -436,19 +436,27 @@ static int launch_wide(const Gemm4Params& p, hipStream_t s) {
 
 // Which kernel, from the host's sizes alone: cap rows over e_local experts make at
 // most `tiles` row tiles of 16.
-//   split: fewer than 3 waves a SIMD if every wave took 16 columns.  One token, H =
-//     4096, F = 1536, gate/up (0.75 waves a SIMD): 11.7 us against 16.5; four tokens
-//     (3): 36.8 against 34.4.  Down, one token (2): 7.4 against 8.0; two (4): 11.9
-//     against 10.7.  Two column tiles a workgroup once those make two workgroups a
-//     CU (gate/up of two tokens 19.9 against 22.9 us, of one 12.8 against 11.7).
+//   split: gate/up below 6.25 waves a SIMD if every wave took 16 columns, down below 3.75.
+//     Where every tile has rows (128 experts, H = 4096, F = 1536, these in us against
+//     wide) gate/up is even from 3 waves on: one token (0.75) 12.7 against 22.1, four (3)
+//     34.0 against 32.5, eight (6) 58 against 57 (H = 2048, F = 768: eight (3) 17.9 against
+//     15.9, twelve (4.5) 21.0 against 19.9); down with its combine of one token (2) 10.5 against
+//     12.4, two (4) 14.8 against 14.1, four (8) 23 against 20 (of three at the smaller sizes (3) 10.1
+//     against 9.7).  On a share of the experts, with room for every pair, most tiles are
+//     empty and wide leaves most waves idle: 32 of 256, H = 7168, F = 2048, gate/up of four
+//     tokens (4) 19 against 41, of sixteen (5) 34 against 47; down of one (3.5) 6.0 against
+//     9.0, four (14) 14.7 against 17.
+//     Two column tiles a workgroup once those make two workgroups a CU (gate/up of two
+//     tokens 19.8 against 22.2 us, of one 13.3 against 12.7).
 //   wide, rows: tiles of 16 up to two rows an expert, of 32 beyond.  128 experts, gate/up
 //     and down: 23 tokens 30 + 16 us with 16 rows, 33 + 18 with 32; 96 tokens (6 rows)
 //     133 + 74 against 128 + 73; 256 tokens (16) 165 + 97 against 147 + 83; 64 rows were
 //     slower at 512 tokens (182 to 218 us for gate/up).
 //   wide, columns of 32-row tiles: 256 a workgroup, which reads the rows half as often,
-//     once that leaves 4 workgroups a CU, else 128.  512 tokens: gate/up 170 against 183
-//     us, down 106 against 118; 64 tokens on 8 experts of 4096 columns (0.75): 52 against
-//     44; 256 tokens on 128 experts of 768 columns (2.3): 45 against 42.
+//     once that leaves 4 workgroups a CU, else 128.  512 tokens on 128 experts, H = 4096,
+//     F = 1536, a skewed router: gate/up 170 against 183 us, down 106 against 118; 64 tokens
+//     on 8 experts of 4096 columns (0.75): 52 against 44; 256 tokens on 128 experts of 768
+//     columns (2.3): 45 against 42.
 //   non-temporal weights (stream): when the packed matrices that the rows can touch
 //     fill half the last-level cache (128 MB) or more, so that they are not there the
 //     next time, for the experts whose rows fit one tile (gemm4_wide).
@@ -462,7 +470,7 @@ static int launch4_rows(Gemm4Params p, hipStream_t s) {
     const int64_t cols = p.N / 16;
     const int64_t tiles = std::min<int64_t>(p.cap, p.cap / 16 + p.e_local);
     const int64_t cus = moe_host::num_cus();
-    if (tiles * cols < 3 * 4 * cus) {
+    if (tiles * cols < (MATS == 2 ? 25 : 15) * cus) {
         if (tiles * cols >= 2 * 2 * cus) return launch_split<MATS, 2, 4>(p, s);
         return launch_split<MATS, 1, 4>(p, s);
     }

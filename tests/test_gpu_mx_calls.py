@@ -115,3 +115,30 @@ def test_save8_on_both_sides_of_its_tile_rule(H, E, rows, F):
                 _lib.moe_grouped_gemm_swiglu_gather_save8(x, src, 1, w[0], w[1], offsets, n)):
         for a, b in zip(got, (h, q, s)):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("Kd,N", [(192, 2112), (1408, 2112)])
+def test_gemm4_of_many_experts_with_a_row_or_two(Kd, N):
+    """16-row tiles of waves with columns of their own, for both products (100 experts of up to three rows, more
+    column tiles than the split kernel takes), with weights that stay in the last-level cache and that do not."""
+    E = 100
+    n = [(5 * i) % 4 if i % 7 else 0 for i in range(E)]
+    off = torch.tensor([0] + n, device="cuda").cumsum(0).to(torch.int32)
+    R = sum(n)
+    assert R <= 2 * E
+    x, w = normal(11, R, Kd), [normal(12 + i, E, Kd, N, std=0.02) for i in range(2)]
+    packed = [_lib.moe_pack4(m) for m in w]
+    del w
+    h = _lib.moe_grouped_gemm4_swiglu(x, None, None, packed[0], packed[1], off, R)
+    c = _lib.moe_grouped_gemm4(x, packed[0], off, R)
+    vals, ends = [_lib.moe_unpack4(*p, Kd) for p in packed], off.tolist()
+    for j in range(E):
+        xr = x[ends[j]:ends[j + 1]].double()
+        a, b = (xr @ v[j].double() for v in vals)
+        # fp32 sums of Kd products, the sigmoid (2^-18 with what follows it) and one rounding to bf16
+        ea, eb = (Kd * 2.0 ** -24 * (xr.abs() @ v[j].double().abs()) for v in vals)
+        assert ((c[ends[j]:ends[j + 1]].double() - a).abs() <= ea + 2.0 ** -8 * a.abs()).all(), j
+        s = torch.sigmoid(a)
+        want = a * s * b
+        tol = 1.1 * ea * b.abs() + (a * s).abs() * eb + 1.1 * ea * eb + (2.0 ** -8 + 2.0 ** -18) * want.abs() + 1e-37
+        assert ((h[ends[j]:ends[j + 1]].double() - want).abs() <= tol).all(), j
