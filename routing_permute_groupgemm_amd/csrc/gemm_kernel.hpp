@@ -1032,9 +1032,9 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
                 // XOR-swizzled by row pair.  Each lane reads the four bytes of its
                 // MFMA-layout columns and widens them there, with the scales of its own
                 // row; (da, db) and then h go out as whole 256-byte row pieces through the
-                // same 8 KiB.  T = 16384, H = 2048, F = 768: 558 us (606 with the bytes widened
-                // before they are staged); T = 131072, H = 7168, F = 2048: 3.65 ms; the bf16
-                // epilogue, which reads twice the bytes and does not write h, 532 us and 3.52.
+                // same 8 KiB.  T = 16384, H = 2048, F = 768: 569 us (5% more with the bytes
+                // widened before they are staged); T = 131072, H = 7168, F = 2048: 3.71 ms; the
+                // bf16 epilogue, which reads twice the bytes and does not write h, 550 us and 3.59.
                 static_assert(TL::kStage / TL::kWaves >= 8192 && BN / WN == 128, "staging space per wave");
                 uint8_t* stg = smem + ((gs + S - 1) % S) * TL::kStage + wave * 8192;
                 const int ln = lane_id_here();
@@ -1481,8 +1481,8 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
             // gathered-row bodies keep the direct stores: their extra per-lane row
             // offsets leave no registers for the staged form, which spilled there.
             // The 8-bit save is staged there too (53 registers spilled, 284 with the
-            // direct form): 6.58 ms against 6.89 with the bf16 save at T = 131072, 0.91
-            // against 0.95 at 16384.
+            // direct form): on gathered rows 6.74 ms against 7.06 with the bf16 save at T =
+            // 131072, H = 7168, F = 2048, 0.91 against 0.95 at 16384, 2048, 768.
             constexpr int kBufs = TL::kStage / TL::kWaves >= 8192 ? 2 : 1;
             uint8_t* stg = smem + ((gs + S - 1) % S) * TL::kStage + wave * (kBufs * 4096);
             const int ln = lane_id_here();
@@ -1505,9 +1505,9 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
             // the staged a or b rows (32 bf16 of a block in 4 lanes) as 8-bit blocks: 64
             // bytes of a row per 8 lanes, and its two scale bytes.  About 45 vector
             // instructions per 8 values, for half the bytes that the bf16 rows take: the
-            // GEMM with it runs 0.9% longer than with the bf16 save (T = 131072, H = 7168,
-            // F = 2048: 6.45 against 6.39 ms; T = 16384, H = 2048, F = 768: 0.89 against
-            // 0.86), where a pass of its own over the saved rows takes 0.24 ms.  Packed
+            // GEMM with it runs 1% longer than with the bf16 save (T = 131072, H = 7168,
+            // F = 2048: 6.62 against 6.54 ms; T = 16384, H = 2048, F = 768: 0.90 against
+            // 0.90), where a pass of its own over the saved rows takes 0.24 ms.  Packed
             // straight from the MFMA layout (a block in lanes l and l ^ 32) the 256-row
             // body spilled 254 registers.
             auto flush8 = [&](int buf, int mt, int half) {
