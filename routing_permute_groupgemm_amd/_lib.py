@@ -4,6 +4,11 @@ Argument marshalling only: torch tensors are checked for dtype/contiguity,
 their device pointers and the current HIP stream are passed through, and a
 negative status becomes a MoeError.  Every computation runs in the HIP
 kernels.  There is no fallback: if the library is missing, loading fails.
+
+stream=: the kernels run on that stream instead of the current one.  The
+arguments have to be ready there, and the results, which come from that
+stream's memory unless their buffers are given, are ready for the current
+stream once it has waited for the other.
 """
 from __future__ import annotations
 
@@ -113,7 +118,7 @@ def _empty(shape, dtype, dev, stream, result=True):
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=dev)
     if result:
-        t.record_stream(torch.cuda.current_stream())
+        t.record_stream(torch.cuda.current_stream(t.device))
     return t
 
 

@@ -162,7 +162,7 @@ def pack_weights4(inp: dict) -> dict:
 def forward4(buf: MoeBuffers, inp: dict):
     """The forward of a decode step on 4-bit weights. inp: device tensors logits and x, and pack_weights4's
     pairs; buffers allocated with weights4=True, whose own capacity holds every local pair (with a smaller one
-    given, the pairs beyond it are dropped and buf.status says so, as in forward)."""
+    given, the pairs beyond it are dropped and buf.status says so, as in forward).  At most 262140 tokens."""
     s = buf.shape
     if not buf.weights4:
         raise _lib.MoeError("forward4: the buffers need weights4=True")

@@ -95,3 +95,22 @@ def test_layer_calls_with_a_workspace_of_their_own(data):
     torch.cuda.synchronize()
     for g in got:
         assert all(torch.equal(p, q) for p, q in zip(g, want))
+
+
+def test_captured_on_a_stream_of_its_own(data):
+    """A call that the captured stream hands to another one, with buffers of its own; replays between eager work."""
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    combine(data, s)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        s.wait_stream(torch.cuda.current_stream())
+        outs = [combine(data, s), combine(data, s)]
+        torch.cuda.current_stream().wait_stream(s)
+    for _ in range(3):
+        for out in outs:
+            out.fill_(7.0)
+        again = combine(data, s)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, data["want"]) for out in outs + [again])

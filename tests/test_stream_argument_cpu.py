@@ -48,7 +48,7 @@ class Traced:
 
         monkeypatch.setattr(torch, "empty", traced_empty)
         monkeypatch.setattr(torch.cuda, "stream", on)
-        monkeypatch.setattr(torch.cuda, "current_stream", lambda: "caller's")
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda device: "caller's")
         monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: self.recorded.add((t.data_ptr(), s)),
                             raising=False)
         monkeypatch.setattr(_lib, "load", Lib)
