@@ -133,19 +133,25 @@ def expert_up(buf: MoeBuffers, w_gate, w_up, x=None):
         _lib.moe_grouped_gemm_swiglu(buf.x_perm, w_gate, w_up, buf.offsets, buf.cap, h=buf.h, ab_save=buf.ab)
 
 
+def _no_weights4(buf, call):
+    if buf.weights4:
+        raise _lib.MoeError(f"{call}: these buffers are for 4-bit weights (forward4)")
+
+
 def expert_down(buf: MoeBuffers, w_down):
+    _no_weights4(buf, "expert_down")
     s = buf.shape
     _lib.moe_grouped_gemm(buf.h, w_down, None, 0, buf.offsets, s.F, s.H, buf.cap, buf.y)
 
 
 def combine(buf: MoeBuffers):
+    _no_weights4(buf, "combine")
     _lib.moe_combine(buf.y, buf.pos, buf.gates, out=buf.out)
 
 
 def forward(buf: MoeBuffers, inp: dict):
     """inp: device tensors logits, x, w_gate, w_up, w_down."""
-    if buf.weights4:
-        raise _lib.MoeError("forward: these buffers are for 4-bit weights (forward4)")
+    _no_weights4(buf, "forward")
     route(buf, inp["logits"])
     permute(buf, inp["x"])
     expert_up(buf, inp["w_gate"], inp["w_up"], inp["x"])
@@ -177,6 +183,8 @@ def forward4(buf: MoeBuffers, inp: dict):
 def backward(buf: MoeBuffers, inp: dict):
     """inp additionally holds d_out (and x, read by the zero-copy weight gradient). Needs the forward's
     ab_save, or its 8-bit (a, b), from which h is recomputed into buf.h (whatever it holds by then)."""
+    if buf.dx is None:
+        raise _lib.MoeError("backward: these buffers were allocated without one")
     s = buf.shape
     H, F, EL, cap = s.H, s.F, s.EL, buf.cap
     _lib.moe_gather_gate_grad(inp["d_out"], buf.pos, buf.gates, buf.y, buf.dy_perm, buf.dgates)

@@ -65,3 +65,14 @@ def test_4bit_buffers_refuse_a_backward():
     for shape, backward in ((SHARE.scaled(T=4, backward=True), None), (SHARE.scaled(T=4), False)):
         buf = pipeline.MoeBuffers.allocate(shape, weights4=True, device="cpu", backward=backward)
         assert buf.dx is None and buf.ab8 is None and not buf.checkpoint8
+
+
+def test_4bit_buffers_refuse_the_steps_of_the_other_forward():
+    """There is no y and no backward in them."""
+    buf = pipeline.MoeBuffers.allocate(SHARE.scaled(T=4), weights4=True, device="cpu")
+    for call in (lambda: pipeline.expert_down(buf, None), lambda: pipeline.combine(buf),
+                 lambda: pipeline.forward(buf, {}), lambda: pipeline.backward(buf, {})):
+        with pytest.raises(_lib.MoeError):
+            call()
+    with pytest.raises(_lib.MoeError):
+        pipeline.backward(pipeline.MoeBuffers.allocate(SHARE.scaled(T=4), device="cpu", backward=False), {})
