@@ -40,7 +40,7 @@ TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic.json")
 CSRC = os.path.join(ROOT, "routing_permute_groupgemm_amd", "csrc")
 # what the GroupGEMM launches of a layer step are compiled from: their translation units and every header of theirs
 GEMM_SRCS = ("gemm_dgrad.hip", "gemm_gather.hip", "gemm_rows.hip", "gemm_swiglu.hip", "gemm_wgrad.hip",
-             "gemm_kernel.hpp", "moe_common.hpp", "mx.hpp")
+             "gemm_kernel.hpp", "linear.hpp", "moe_common.hpp", "mx.hpp")
 
 
 def parse():

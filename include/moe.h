@@ -499,6 +499,112 @@ int moe_grouped_gemm4_combine(const moe_bf16* a, const uint8_t* q4, const uint8_
                               moe_stream stream);
 
 /*
+ * A whole layer for a few tokens: routing, the local experts and the combine of
+ * a decode step on bf16 weights, in two launches.
+ *   topk_idx, gates as moe_route writes them (bit for bit);
+ *   out[t] = bf16( residual[t] + sum over k ascending, e = topk_idx[t,k] local, of gates[t,k] * (h . w_down[j]) )
+ *   h = bf16(silu(x[t] . w_gate[j]) * (x[t] . w_up[j])),   j = e - e_begin
+ * with fp32 sums and one rounding of out; a token without a local expert gets
+ * its residual, or +0.  A token's bits do not depend on the other tokens' values.
+ *   logits fp32 [T,E];  x bf16 [T,H];  w_gate, w_up bf16 [e_local,H,F];
+ *   w_down bf16 [e_local,F,H];  residual bf16 [T,H] or NULL (it may be out);
+ *   topk_idx int32 [T,K], gates fp32 [T,K], out bf16 [T,H] out;
+ *   ws: device workspace of at least moe_layer_few_workspace_size(T, K, e_local,
+ *   H, F) bytes, which the call initialises itself; one for each of calls that
+ *   may overlap (graphs that are replayed at once among them).
+ * T <= MOE_FEW_TOKENS and e_begin + e_local <= E (MOE_EINVAL); other limits and
+ * errors as moe_route and moe_grouped_gemm_swiglu.  Every weight of an expert
+ * that has a token is read once, so it is the faster form while the tokens are
+ * few; pipeline.forward takes any number of them.
+ */
+#define MOE_FEW_TOKENS 64
+size_t moe_layer_few_workspace_size(int T, int K, int e_local, int H, int F);
+int moe_layer_few(const float* logits, const moe_bf16* x, int T, int E, int K, int e_begin, int e_local,
+                  const moe_bf16* w_gate, const moe_bf16* w_up, const moe_bf16* w_down, int H, int F,
+                  const moe_bf16* residual, int32_t* topk_idx, float* gates, moe_bf16* out, void* ws, size_t ws_bytes,
+                  moe_stream stream);
+
+/*
+ * Layer norm of the tokens (what the router and the experts read), with the
+ * residual stream's addition in front of it.  For every row:
+ *   s = x + add, rounded to the type of x;   mean = sum(s) / H;   rstd = 1 / sqrt(sum((s - mean)^2) / H + eps)
+ *   y = bf16( (s - mean) * rstd * weight + bias )
+ *   rms = 1: the same with mean 0 (the root mean square), mean not written.
+ *   x [T,H], bf16, or fp32 with x_f32 = 1;  add bf16 [T,H] or NULL (0);
+ *   weight, bias fp32 [H] or NULL (1 and 0);
+ *   sum [T,H] out, of the type of x, or NULL: s, which the backward reads (it may be x);
+ *   y bf16 [T,H] out;  mean, rstd fp32 [T] out, or NULL.
+ * H a multiple of 64 (MOE_ESHAPE) up to 16384, eps >= 0 (MOE_EINVAL).
+ */
+int moe_layer_norm(const void* x, int x_f32, const moe_bf16* add, int T, int H, const float* weight,
+                   const float* bias, float eps, int rms, void* sum, moe_bf16* y, float* mean, float* rstd,
+                   moe_stream stream);
+
+/*
+ * Its backward.  With xh = (s - mean) * rstd and g = dy * weight, for every row:
+ *   dx = rstd * (g - sum(g)/H - xh * sum(g * xh)/H) + d_sum     (rms: without sum(g)/H)
+ *   dw = sum over rows of dy * xh,   db = sum over rows of dy   (fp32, in an order that the sizes and the GPU's
+ *   number of CUs decide)
+ * dx is the gradient of x, and of add: d_sum, the gradient that reaches s past
+ * the norm, is added to it before the one rounding.
+ *   dy bf16 [T,H];  s [T,H] (x, or the forward's sum) and d_sum [T,H] or NULL, bf16, or
+ *   fp32 with x_f32 = 1;  weight as the forward;  mean, rstd fp32 [T] from it (mean not read with rms = 1);
+ *   dx [T,H] out, of the type of s (it may be d_sum);  dw, db fp32 [H] out, or NULL (db is
+ *   NULL with rms = 1: MOE_EINVAL);
+ *   ws: device workspace of at least moe_layer_norm_backward_workspace_size(T, H)
+ *   bytes if dw or db is wanted, one for each of calls that may overlap.
+ * T = 0 writes zeros to dw and db.
+ */
+size_t moe_layer_norm_backward_workspace_size(int T, int H);
+int moe_layer_norm_backward(const moe_bf16* dy, const void* s, int x_f32, int T, int H, const float* weight,
+                            const float* mean, const float* rstd, int rms, const void* d_sum, void* dx, float* dw,
+                            float* db, void* ws, size_t ws_bytes, moe_stream stream);
+
+enum moe_act {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_RELU = 1,  /* max(z, 0) */
+    MOE_ACT_SILU = 2,  /* z / (1 + exp(-z)) */
+    MOE_ACT_GELU = 3   /* z * (1 + erf(z / sqrt(2))) / 2 */
+};
+
+/*
+ * Dense product with bias, activation and residual in its epilogue, for the
+ * products that do not go by expert (a shared expert's down product onto the
+ * routed output, a dense feed-forward layer):
+ *   z = x . w + bias   (fp32 accumulate),   y = bf16(act(z) + residual)
+ *   x bf16 [T,Kd];  w bf16 [Kd,N];  bias fp32 [N] or NULL;  act a moe_act;
+ *   residual bf16 [T,N] or NULL (it may be y);
+ *   z bf16 [T,N] out or NULL: z rounded, for the backward;  y bf16 [T,N] out;
+ *   ws: device workspace of at least moe_linear_workspace_size(T, Kd, N) bytes
+ *   (may be NULL when that is 0), one for each of calls that may overlap.
+ * Kd and N multiples of 64 (MOE_ESHAPE); Kd * N * 2 < 2^31, 256 rows of x and y
+ * below 2 GiB, T <= 2^30 (MOE_EINVAL).  Where the columns are too few to fill
+ * the GPU the contraction is cut into chunks whose fp32 partials are added in
+ * chunk order: the order of a sum goes by the sizes and the GPU's number of CUs.
+ */
+size_t moe_linear_workspace_size(int T, int Kd, int N);
+int moe_linear(const moe_bf16* x, int T, int Kd, const moe_bf16* w, int N, const float* bias, int act,
+               const moe_bf16* residual, moe_bf16* z, moe_bf16* y, void* ws, size_t ws_bytes, moe_stream stream);
+
+/*
+ * Its backward, from dy (which is the residual's gradient as it is):
+ *   dz = bf16(dy * act'(z)), at the saved z;    db = sum over rows of dy * act'(z)   (fp32, before that rounding)
+ *   dx = bf16(dz . w^T),    dw = x^T . dz       (fp32 accumulate)
+ * With MOE_ACT_NONE dz is dy: z is not read and dz not written.
+ *   dy bf16 [T,N];  x, w as the forward (x may be NULL without dw, w without dx);  z bf16 [T,N];
+ *   dz bf16 [T,N] out (required with an activation; it may be dy);  dx bf16
+ *   [T,Kd] out or NULL;  dw fp32 [Kd,N] out or NULL;  db fp32 [N] out or NULL;
+ *   ws: device workspace of at least moe_linear_backward_workspace_size(T, Kd, N)
+ *   bytes if dw or db is wanted, one for each of calls that may overlap.
+ * dw and db sum the rows in fixed chunks added in chunk order.  T = 0 writes
+ * zeros to dw and db.  Limits as moe_linear.
+ */
+size_t moe_linear_backward_workspace_size(int T, int Kd, int N);
+int moe_linear_backward(const moe_bf16* dy, const moe_bf16* x, int T, int Kd, const moe_bf16* w, int N, int act,
+                        const moe_bf16* z, moe_bf16* dz, moe_bf16* dx, float* dw, float* db, void* ws,
+                        size_t ws_bytes, moe_stream stream);
+
+/*
  * Measurement aid, not a step of the layer: the bf16 MFMA rate this GPU
  * sustains.  Each of the blocks x 4 waves keeps its own 8 fragments of
  * operands in registers and runs iters rounds of a 4 x 4 block of

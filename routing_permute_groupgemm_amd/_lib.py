@@ -23,6 +23,7 @@ _p = ctypes.c_void_p
 _i = ctypes.c_int
 _z = ctypes.c_size_t
 _i64 = ctypes.c_int64
+_f = ctypes.c_float
 
 # every symbol declared in include/moe.h, with its ctypes signature
 SIGNATURES = {
@@ -58,6 +59,15 @@ SIGNATURES = {
     "moe_grouped_gemm4": ([_p, _p, _p, _p, _i, _i, _i, _i, _p, _p], _i),
     "moe_gemm4_combine_workspace_size": ([_i, _i], _z),
     "moe_grouped_gemm4_combine": ([_p, _p, _p, _p, _i, _i, _i, _i, _p, _p, _i, _i, _p, _p, _p, _z, _p], _i),
+    "moe_layer_few_workspace_size": ([_i, _i, _i, _i, _i], _z),
+    "moe_layer_few": ([_p, _p, _i, _i, _i, _i, _i, _p, _p, _p, _i, _i, _p, _p, _p, _p, _p, _z, _p], _i),
+    "moe_layer_norm": ([_p, _i, _p, _i, _i, _p, _p, _f, _i, _p, _p, _p, _p, _p], _i),
+    "moe_layer_norm_backward_workspace_size": ([_i, _i], _z),
+    "moe_layer_norm_backward": ([_p, _p, _i, _i, _i, _p, _p, _p, _i, _p, _p, _p, _p, _p, _z, _p], _i),
+    "moe_linear_workspace_size": ([_i, _i, _i], _z),
+    "moe_linear": ([_p, _i, _i, _p, _i, _p, _i, _p, _p, _p, _p, _z, _p], _i),
+    "moe_linear_backward_workspace_size": ([_i, _i, _i], _z),
+    "moe_linear_backward": ([_p, _p, _i, _i, _p, _i, _i, _p, _p, _p, _p, _p, _p, _z, _p], _i),
     "moe_probe_mfma": ([_p, _i, _i, _p, _p], _i),
     "moe_probe_mfma16": ([_p, _i, _i, _p, _p], _i),
     "moe_probe_copy": ([_p, _p, _i64, _i, _i, _p], _i),
@@ -65,6 +75,8 @@ SIGNATURES = {
 
 MOE_EPI_NONE = 0
 MOE_EPI_SWIGLU_BWD = 1
+MOE_FEW_TOKENS = 64
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}  # moe_act
 
 _lib = None
 
@@ -816,6 +828,190 @@ def moe_grouped_gemm4_combine(a, w, offsets, cap_rows, pos, gates, y=None, out=N
                                             _ptr(pos), _ptr(gates), T, K, _ptr(y), _ptr(out), _ptr(ws), ws.numel(),
                                             _handle(stream, dev)))
     return out
+
+
+def _ws(ws, need, dev, stream):
+    """The caller's workspace, or a new one where there is none or it is too small (None if none is needed)."""
+    if ws is not None:
+        _arg(ws, torch.uint8, "ws", dev)
+    if need == 0 or (ws is not None and ws.numel() >= need):
+        return ws, 0 if ws is None else ws.numel()
+    return _empty(need, torch.uint8, dev, stream, result=False), need
+
+
+def _rank2(t, name):
+    if t.dim() != 2:
+        raise MoeError(f"{name}: expected 2 dimensions, got {tuple(t.shape)}")
+    return t.shape
+
+
+def _given(t, shape, dtype, name, dev):
+    """An optional input: None, or a tensor of exactly this shape."""
+    if t is not None:
+        _arg(t, dtype, name, dev)
+        _shape(t, shape, name)
+    return _ptr(t)
+
+
+def moe_layer_few_workspace_size(T, K, e_local, H, F) -> int:
+    return int(load().moe_layer_few_workspace_size(T, K, e_local, H, F))
+
+
+def moe_layer_few(logits, x, K, e_begin, w_gate, w_up, w_down, residual=None, topk_idx=None, gates=None, out=None,
+                  ws=None, stream=None):
+    """The whole layer for at most MOE_FEW_TOKENS tokens on the experts e_begin .. e_begin + e_local - 1 (bf16 weights
+    [e_local, H, F] and [e_local, F, H]) -> (out [T, H], topk_idx, gates); residual is added before the one rounding."""
+    dev = _device(stream, logits)
+    _arg(logits, torch.float32, "logits", dev)
+    for t, name in ((x, "x"), (w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down")):
+        _arg(t, torch.bfloat16, name, dev)
+    T, E = _rank2(logits, "logits")
+    if w_gate.dim() != 3:
+        raise MoeError(f"w_gate: expected [E, H, F], got {tuple(w_gate.shape)}")
+    EL, H, F = w_gate.shape
+    _shape(w_up, (EL, H, F), "w_up")
+    _shape(w_down, (EL, F, H), "w_down")
+    _shape(x, (T, H), "x")
+    res = _given(residual, (T, H), torch.bfloat16, "residual", dev)
+    K = int(K)
+    topk_idx = _out(topk_idx, (T, max(K, 0)), torch.int32, "topk_idx", dev, stream)
+    gates = _out(gates, (T, max(K, 0)), torch.float32, "gates", dev, stream)
+    out = _out(out, (T, H), torch.bfloat16, "out", dev, stream)
+    lib = load()
+    ws, size = _ws(ws, lib.moe_layer_few_workspace_size(T, K, EL, H, F), dev, stream)
+    _check(lib.moe_layer_few(_ptr(logits), _ptr(x), T, E, K, e_begin, EL, _ptr(w_gate), _ptr(w_up), _ptr(w_down), H, F,
+                             res, _ptr(topk_idx), _ptr(gates), _ptr(out), _ptr(ws), size, _handle(stream, dev)))
+    return out, topk_idx, gates
+
+
+def _stream_type(t, name, dev):
+    """The residual stream's type: bf16 (0) or fp32 (1)."""
+    f32 = t.dtype is torch.float32
+    _arg(t, torch.float32 if f32 else torch.bfloat16, name, dev)
+    return int(f32)
+
+
+def moe_layer_norm(x, weight=None, bias=None, add=None, eps=1e-5, rms=False, sum=None, y=None, mean=None, rstd=None,
+                   stream=None):
+    """s = x + add and y = bf16((s - mean) * rstd * weight + bias), or of the root mean square with rms -> (s, y, mean,
+    rstd); s is x itself without add (and sum), mean is None with rms.  x: bf16 or fp32 [T, H]; sum may be x."""
+    dev = _device(stream, x)
+    f32 = _stream_type(x, "x", dev)
+    T, H = _rank2(x, "x")
+    w = _given(weight, (H,), torch.float32, "weight", dev)
+    b = _given(bias, (H,), torch.float32, "bias", dev)
+    a = _given(add, (T, H), torch.bfloat16, "add", dev)
+    if rms and mean is not None:
+        raise MoeError("mean: there is none with rms")
+    if add is not None or sum is not None:
+        sum = _out(sum, (T, H), x.dtype, "sum", dev, stream)
+    y = _out(y, (T, H), torch.bfloat16, "y", dev, stream)
+    if not rms:
+        mean = _out(mean, (T,), torch.float32, "mean", dev, stream)
+    rstd = _out(rstd, (T,), torch.float32, "rstd", dev, stream)
+    _check(load().moe_layer_norm(_ptr(x), f32, a, T, H, w, b, eps, int(rms), _ptr(sum), _ptr(y), _ptr(mean),
+                                 _ptr(rstd), _handle(stream, dev)))
+    return (x if sum is None else sum), y, mean, rstd
+
+
+def moe_layer_norm_backward_workspace_size(T, H) -> int:
+    return int(load().moe_layer_norm_backward_workspace_size(T, H))
+
+
+def moe_layer_norm_backward(dy, s, weight, mean, rstd, d_sum=None, rms=False, want_dw=True, want_db=None, dx=None,
+                            dw=None, db=None, ws=None, stream=None):
+    """-> (dx of the type of s, dw, db fp32 [H]; None where not wanted: want_db defaults to there being a mean).
+    d_sum, of the type of s, is added to dx, which may be d_sum itself."""
+    dev = _device(stream, dy)
+    _arg(dy, torch.bfloat16, "dy", dev)
+    f32 = _stream_type(s, "s", dev)
+    T, H = _rank2(s, "s")
+    _shape(dy, (T, H), "dy")
+    w = _given(weight, (H,), torch.float32, "weight", dev)
+    if rstd is None or (mean is None and not rms):
+        raise MoeError("the backward needs the forward's rstd, and its mean unless rms is set")
+    m = None if rms else _given(mean, (T,), torch.float32, "mean", dev)
+    r = _given(rstd, (T,), torch.float32, "rstd", dev)
+    d = _given(d_sum, (T, H), s.dtype, "d_sum", dev)
+    want_db = (not rms) if want_db is None else want_db
+    if rms and (want_db or db is not None):
+        raise MoeError("db: there is no bias with rms")
+    dx = _out(dx, (T, H), s.dtype, "dx", dev, stream)
+    dw = _out(dw, (H,), torch.float32, "dw", dev, stream) if want_dw or dw is not None else None
+    db = _out(db, (H,), torch.float32, "db", dev, stream) if want_db or db is not None else None
+    lib = load()
+    need = lib.moe_layer_norm_backward_workspace_size(T, H) if dw is not None or db is not None else 0
+    ws, size = _ws(ws, need, dev, stream)
+    _check(lib.moe_layer_norm_backward(_ptr(dy), _ptr(s), f32, T, H, w, m, r, int(rms), d, _ptr(dx), _ptr(dw),
+                                       _ptr(db), _ptr(ws), size, _handle(stream, dev)))
+    return dx, dw, db
+
+
+def _act(act):
+    if act not in ACTS:
+        raise MoeError(f"act: expected one of {', '.join(ACTS)}, got {act!r}")
+    return ACTS[act]
+
+
+def moe_linear_workspace_size(T, Kd, N) -> int:
+    return int(load().moe_linear_workspace_size(T, Kd, N))
+
+
+def moe_linear(x, w, bias=None, act="none", residual=None, want_z=False, z=None, y=None, ws=None, stream=None):
+    """y = bf16(act(x . w + bias) + residual) -> (y, z), z the bf16 pre-activation if wanted (or its buffer given), else
+    None.  x bf16 [T, Kd], w bf16 [Kd, N], bias fp32 [N], act one of ACTS; residual bf16 [T, N] may be y."""
+    dev = _device(stream, x)
+    _arg(x, torch.bfloat16, "x", dev)
+    _arg(w, torch.bfloat16, "w", dev)
+    T, Kd = _rank2(x, "x")
+    N = _rank2(w, "w")[1]
+    _shape(w, (Kd, N), "w")
+    b = _given(bias, (N,), torch.float32, "bias", dev)
+    res = _given(residual, (T, N), torch.bfloat16, "residual", dev)
+    code = _act(act)
+    z = _out(z, (T, N), torch.bfloat16, "z", dev, stream) if want_z or z is not None else None
+    y = _out(y, (T, N), torch.bfloat16, "y", dev, stream)
+    lib = load()
+    ws, size = _ws(ws, lib.moe_linear_workspace_size(T, Kd, N), dev, stream)
+    _check(lib.moe_linear(_ptr(x), T, Kd, _ptr(w), N, b, code, res, _ptr(z), _ptr(y), _ptr(ws), size,
+                          _handle(stream, dev)))
+    return y, z
+
+
+def moe_linear_backward_workspace_size(T, Kd, N) -> int:
+    return int(load().moe_linear_backward_workspace_size(T, Kd, N))
+
+
+def moe_linear_backward(dy, x, w, act="none", z=None, want_dx=True, want_dw=True, want_db=True, dz=None, dx=None,
+                        dw=None, db=None, ws=None, stream=None):
+    """-> (dz, dx bf16, dw fp32 [Kd, N], db fp32 [N]; None where not wanted).  dz is dy itself without an activation;
+    with one, z is the forward's, and dz may be given (dy itself too)."""
+    dev = _device(stream, dy)
+    for t, name in ((dy, "dy"), (x, "x"), (w, "w")):
+        _arg(t, torch.bfloat16, name, dev)
+    T, Kd = _rank2(x, "x")
+    N = _rank2(w, "w")[1]
+    _shape(w, (Kd, N), "w")
+    _shape(dy, (T, N), "dy")
+    code = _act(act)
+    if code:
+        if z is None:
+            raise MoeError("z: the backward of an activation needs the forward's")
+        zp = _given(z, (T, N), torch.bfloat16, "z", dev)
+        dz = _out(dz, (T, N), torch.bfloat16, "dz", dev, stream)
+    else:
+        if dz is not None and dz is not dy:
+            raise MoeError("dz: it is dy itself without an activation")
+        zp, dz = None, None
+    dx = _out(dx, (T, Kd), torch.bfloat16, "dx", dev, stream) if want_dx or dx is not None else None
+    dw = _out(dw, (Kd, N), torch.float32, "dw", dev, stream) if want_dw or dw is not None else None
+    db = _out(db, (N,), torch.float32, "db", dev, stream) if want_db or db is not None else None
+    lib = load()
+    need = lib.moe_linear_backward_workspace_size(T, Kd, N) if dw is not None or db is not None else 0
+    ws, size = _ws(ws, need, dev, stream)
+    _check(lib.moe_linear_backward(_ptr(dy), _ptr(x), T, Kd, _ptr(w), N, code, zp, _ptr(dz), _ptr(dx), _ptr(dw),
+                                   _ptr(db), _ptr(ws), size, _handle(stream, dev)))
+    return (dy if dz is None else dz), dx, dw, db
 
 
 def moe_probe_mfma(operands, iters, out=None, stream=None):

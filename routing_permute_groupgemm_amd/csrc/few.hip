@@ -1,0 +1,367 @@
+// A whole layer for a few tokens in two kernels: what a decode step on bf16
+// weights runs instead of the routing, the permutation, two GroupGEMMs and the
+// combine.
+//
+//   out[t] = bf16(residual[t] + sum over k ascending of gate[t,k] * y[t,k])
+//   y[t,k] = bf16(silu(x_t . Wg_j) * (x_t . Wu_j)) . Wd_j,   j = the k-th expert of token t, if it is local
+// Almost every byte is a weight of an expert that has a token, read once (6*H*F
+// bytes each): the time is that of streaming them.
+//
+//   few_up    every workgroup routes the T tokens itself (T <= 64, so an expert's
+//             tokens are a 64-bit mask and a token's row among them a popcount), then
+//             takes blocks of 64 columns of gate and up of the experts that have
+//             tokens.  Its waves take the contraction's steps in turn; their sums
+//             meet in LDS, in wave order.  Workgroup 0 also writes the choices, the
+//             gates and the plan that the second kernel reads, and clears its counters.
+//   few_down  a workgroup takes 128 columns of an expert's down product, fp32 rows in
+//             the workspace; the last of a column block's workgroups to finish
+//             forms the tokens' gated sums there, so no third launch is needed.
+//             Which one that is does not change what is added in which order.
+// A row's bits do not depend on the other tokens of the call.
+#include "rows_stream.hpp"
+#include "route_select.hpp"
+
+using moe_host::misaligned;
+
+namespace moe {
+
+constexpr int kFewT = 64;
+constexpr int kFewGroups = 512;
+constexpr int kFewUpCols = 64, kFewDownCols = 128;
+
+// An expert with tokens: its rows row0 .. row0+rows-1 of the expert-grouped order.
+struct FewExpert {
+    int j, row0, rows, pad;
+};
+
+struct FewParams {
+    const float* logits;
+    const uint16_t* x;
+    int T, E, K, e_begin, e_local;
+    const uint16_t *w_gate, *w_up, *w_down;
+    int H, F;
+    const uint16_t* residual;
+    int32_t* topk_idx;
+    float* gates;
+    uint16_t* out;
+    // workspace
+    int* n_active;
+    int* arrived;       // [column blocks of the down product]
+    FewExpert* active;  // [min(e_local, T*K)]
+    int* pos;           // [T*K]: the pair's row, or -1
+    uint16_t* h;        // [rows][F]
+    float* y;           // [rows][H]
+};
+
+template <int EPL>
+__device__ __forceinline__ void choose(const float* row, int E, int K, int lane, int& idx, float& score, float& s_max) {
+    uint32_t key[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        const int e = i * 64 + lane;
+        key[i] = e < E ? score_key(row[e]) : 0u;
+    }
+    select_rounds<EPL>(key, K, lane, idx, score, s_max);
+}
+
+struct FewPlan {
+    unsigned long long mask[kFewGroups];  // tokens of a local expert
+    uint16_t expert[kFewGroups];          // the experts that have tokens, ascending
+    uint16_t row0[kFewGroups];            // their first rows
+    uint16_t start[kFewGroups];           // a local expert's first row
+    int16_t local[kFewT * 16];            // a pair's local expert, or -1
+    uint8_t token[kFewT * 16];            // a row's token
+    int n_active;
+};
+
+// Routing of all tokens by this workgroup of W waves, into `s`; the workgroup `write` also writes the call's outputs
+// and the plan.
+template <int W>
+__device__ __forceinline__ void route_few(const FewParams& p, FewPlan& s, bool write) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    for (int j = tid; j < p.e_local; j += 64 * W) s.mask[j] = 0ull;
+    __syncthreads();
+    for (int t = wave; t < p.T; t += W) {
+        const float* row = p.logits + (int64_t)t * p.E;
+        int idx = 0;
+        float score = 0.0f, s_max = 0.0f;
+        if (p.E <= 64) choose<1>(row, p.E, p.K, lane, idx, score, s_max);
+        else if (p.E <= 128) choose<2>(row, p.E, p.K, lane, idx, score, s_max);
+        else if (p.E <= 256) choose<4>(row, p.E, p.K, lane, idx, score, s_max);
+        else choose<8>(row, p.E, p.K, lane, idx, score, s_max);
+        if (write) {
+            const float ex = lane < p.K ? expf(score - s_max) : 0.0f;
+            float z = 0.0f;
+            for (int k = 0; k < p.K; ++k) z += __shfl(ex, k, 64);
+            if (lane < p.K) {
+                p.topk_idx[t * p.K + lane] = idx;
+                p.gates[t * p.K + lane] = ex / z;
+            }
+        }
+        if (lane < p.K) {
+            const int j = idx - p.e_begin;
+            const bool in = j >= 0 && j < p.e_local;
+            s.local[t * p.K + lane] = in ? (int16_t)j : (int16_t)-1;
+            if (in) atomicOr(&s.mask[j], 1ull << t);
+        }
+    }
+    __syncthreads();
+    if (wave == 0) {  // lane l: experts 8l .. 8l+7
+        int rows = 0, used = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = lane * 8 + i;
+            const int n = j < p.e_local ? __popcll(s.mask[j]) : 0;
+            rows += n;
+            used += n > 0;
+        }
+        int r = rows, u = used;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int a = __shfl_up(r, o, 64), b = __shfl_up(u, o, 64);
+            if (lane >= o) {
+                r += a;
+                u += b;
+            }
+        }
+        if (lane == 63) s.n_active = u;
+        r -= rows;
+        u -= used;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = lane * 8 + i;
+            const int n = j < p.e_local ? __popcll(s.mask[j]) : 0;
+            if (j < p.e_local) s.start[j] = (uint16_t)r;
+            if (n > 0) {
+                s.expert[u] = (uint16_t)j;
+                s.row0[u] = (uint16_t)r;
+                if (write) p.active[u] = FewExpert{j, r, n, 0};
+                ++u;
+                r += n;
+            }
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < p.T * p.K; i += 64 * W) {
+        const int j = s.local[i], t = i / p.K;
+        int row = -1;
+        if (j >= 0) {
+            row = s.start[j] + __popcll(s.mask[j] & ((1ull << t) - 1ull));
+            s.token[row] = (uint8_t)t;
+        }
+        if (write) p.pos[i] = row;
+    }
+    if (write) {
+        if (tid == 0) *p.n_active = s.n_active;
+        for (int i = tid; i < (p.H + kFewDownCols - 1) / kFewDownCols; i += 64 * W) p.arrived[i] = 0;
+    }
+    __syncthreads();
+}
+
+template <int MT, int S, int W, bool NTL>
+__global__ __launch_bounds__(64 * W) void few_up(FewParams p) {
+    __shared__ FewPlan plan;
+    __shared__ __attribute__((aligned(16))) WaveSums<2, 4, W> sums;
+    route_few<W>(p, plan, blockIdx.x == 0);
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int slabs = p.F / kFewUpCols;
+    const int total = plan.n_active * slabs;
+    for (int id = blockIdx.x; id < total; id += gridDim.x) {
+        const int a = id / slabs, col0 = (id - a * slabs) * kFewUpCols;
+        const int j = __builtin_amdgcn_readfirstlane((int)plan.expert[a]);
+        const int row0 = __builtin_amdgcn_readfirstlane((int)plan.row0[a]);
+        const int rows = __builtin_amdgcn_readfirstlane(__popcll(plan.mask[j]));
+        uint32_t x_at[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            x_at[m] = (uint32_t)plan.token[row0 + min(16 * m + (lane & 15), rows - 1)] * (uint32_t)(p.H * 2);
+        const int64_t at = (int64_t)j * p.H * p.F;
+        const uint16_t* const w[2] = {p.w_gate + at, p.w_up + at};
+        RowStream<2, 4, MT, S, NTL> r;
+        r.run(w, p.F, col0 + 4 * (lane & 15), p.x, x_at, rows, wave, W, p.H / 32);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            if (16 * m >= rows) break;
+            __syncthreads();  // the sums of the block before are read
+            sums.put(r, m, wave, lane);
+            __syncthreads();
+            for (int i = tid; i < 256; i += 64 * W) {
+                const int row = i >> 4, c = (i & 15) * 4;
+                if (16 * m + row >= rows) continue;
+                const f32x4 g = sums.get(row, c), u = sums.get(row, 64 + c);
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = silu_f(g[e]) * u[e];
+                *(u32x2*)(p.h + (int64_t)(row0 + 16 * m + row) * p.F + col0 + c) =
+                    u32x2{pack_bf2x(v[0], v[1]), pack_bf2x(v[2], v[3])};
+            }
+        }
+    }
+}
+
+// The gated sums of columns col0 .. col0+127 of every token.
+template <int W>
+__device__ __forceinline__ void combine_few(const FewParams& p, int col0) {
+    const int cols = min(kFewDownCols, p.H - col0) / 4;
+    for (int i = threadIdx.x; i < p.T * (kFewDownCols / 4); i += 64 * W) {
+        const int t = i / (kFewDownCols / 4), c = i % (kFewDownCols / 4);
+        if (c >= cols) continue;
+        const int n = col0 + 4 * c;
+        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int k = 0; k < p.K; ++k) {
+            const int r = p.pos[t * p.K + k];
+            if (r >= 0) acc += p.gates[t * p.K + k] * *(const f32x4*)(p.y + (int64_t)r * p.H + n);
+        }
+        if (p.residual) {
+            const u32x2 v = *(const u32x2*)(p.residual + (int64_t)t * p.H + n);
+            acc += f32x4{bf_lo(v[0]), bf_hi(v[0]), bf_lo(v[1]), bf_hi(v[1])};
+        }
+        *(u32x2*)(p.out + (int64_t)t * p.H + n) = u32x2{pack_bf2x(acc[0], acc[1]), pack_bf2x(acc[2], acc[3])};
+    }
+}
+
+template <int MT, int S, int W, bool NTL>
+__global__ __launch_bounds__(64 * W) void few_down(FewParams p) {
+    __shared__ __attribute__((aligned(16))) WaveSums<1, 8, W> sums;
+    __shared__ int s_last;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int slabs = (p.H + kFewDownCols - 1) / kFewDownCols;
+    const int n_active = *p.n_active;
+    const int a = (int)blockIdx.x / slabs, slab = (int)blockIdx.x % slabs, col0 = slab * kFewDownCols;
+    if (a >= n_active) {
+        // no pair is local: the sums are empty
+        if (n_active == 0 && a == 0) combine_few<W>(p, col0);
+        return;
+    }
+    const FewExpert e = p.active[a];
+    const int j = __builtin_amdgcn_readfirstlane(e.j), row0 = __builtin_amdgcn_readfirstlane(e.row0);
+    const int rows = __builtin_amdgcn_readfirstlane(e.rows);
+    uint32_t x_at[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) x_at[m] = (uint32_t)(row0 + min(16 * m + (lane & 15), rows - 1)) * (uint32_t)(p.F * 2);
+    const uint16_t* const w[1] = {p.w_down + (int64_t)j * p.F * p.H};
+    RowStream<1, 8, MT, S, NTL> r;
+    // columns past the last are read as the last ones; their sums are not stored
+    r.run(w, p.H, min(col0 + 8 * (lane & 15), p.H - 8), p.h, x_at, rows, wave, W, p.F / 32);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        if (16 * m >= rows) break;
+        if (m > 0) __syncthreads();
+        sums.put(r, m, wave, lane);
+        __syncthreads();
+        for (int i = tid; i < 512; i += 64 * W) {
+            const int row = i >> 5, c = (i & 31) * 4;
+            if (16 * m + row < rows && col0 + c < p.H)
+                *(f32x4*)(p.y + (int64_t)(row0 + 16 * m + row) * p.H + col0 + c) = sums.get(row, c);
+        }
+    }
+    // The last of the column block's workgroups sees every other's rows: each makes its own visible to the whole
+    // GPU before it counts itself, and the last one reads after it has seen the full count.
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) s_last = atomicAdd(p.arrived + slab, 1) == n_active - 1;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    combine_few<W>(p, col0);
+}
+
+struct FewSizes {
+    size_t arrived, active, pos, h, y, total;
+};
+static size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+
+static FewSizes few_sizes(int T, int K, int e_local, int H, int F) {
+    const size_t rows = (size_t)T * std::min(K, e_local);
+    FewSizes s{};
+    s.arrived = 256;
+    s.active = s.arrived + up256((size_t)(H + kFewDownCols - 1) / kFewDownCols * 4);
+    s.pos = s.active + up256(std::min<size_t>(e_local, rows) * sizeof(FewExpert));
+    s.h = s.pos + up256((size_t)T * K * 4);
+    s.y = s.h + up256(rows * F * 2);
+    s.total = s.y + up256(rows * H * 4);
+    return s;
+}
+
+static int few_check(int T, int E, int K, int e_local, int H, int F) {
+    if (T < 0 || T > kFewT || E < 1 || E > 512 || K < 1 || K > 16 || e_local < 0 || e_local > kFewGroups || H <= 0 ||
+        F <= 0)
+        return MOE_EINVAL;
+    if (K > E || H % 64 || F % 64) return MOE_ESHAPE;
+    if ((int64_t)H * F * 2 >= (1ll << 31) || H > (1 << 24) || F > (1 << 20)) return MOE_EINVAL;
+    return MOE_OK;
+}
+
+template <int MT, int S>
+static int launch_few(const FewParams& p, bool ntl, hipStream_t s) {
+    constexpr int W = 4;
+    const int experts = std::min(p.e_local, p.T * p.K);
+    const int64_t up = std::max<int64_t>(1, std::min<int64_t>((int64_t)experts * (p.F / kFewUpCols), 3 * moe_host::num_cus()));
+    const int64_t down = (int64_t)std::max(experts, 1) * ((p.H + kFewDownCols - 1) / kFewDownCols);
+    if (ntl) few_up<MT, S, W, true><<<(unsigned)up, 64 * W, 0, s>>>(p);
+    else few_up<MT, S, W, false><<<(unsigned)up, 64 * W, 0, s>>>(p);
+    const int rc = moe_host::launch_status();
+    if (rc != MOE_OK) return rc;
+    if (ntl) few_down<MT, S, W, true><<<(unsigned)down, 64 * W, 0, s>>>(p);
+    else few_down<MT, S, W, false><<<(unsigned)down, 64 * W, 0, s>>>(p);
+    return moe_host::launch_status();
+}
+
+}  // namespace moe
+
+extern "C" size_t moe_layer_few_workspace_size(int T, int K, int e_local, int H, int F) {
+    using namespace moe;
+    if (few_check(T, 512, K, e_local, H, F) != MOE_OK || T == 0) return 0;
+    return few_sizes(T, K, e_local, H, F).total;
+}
+
+extern "C" int moe_layer_few(const float* logits, const moe_bf16* x, int T, int E, int K, int e_begin, int e_local,
+                             const moe_bf16* w_gate, const moe_bf16* w_up, const moe_bf16* w_down, int H, int F,
+                             const moe_bf16* residual, int32_t* topk_idx, float* gates, moe_bf16* out, void* ws,
+                             size_t ws_bytes, moe_stream stream) {
+    using namespace moe;
+    const int rc = few_check(T, E, K, e_local, H, F);
+    if (rc != MOE_OK) return rc;
+    if (e_begin < 0 || e_begin > E - e_local) return MOE_EINVAL;
+    if (T == 0) return MOE_OK;
+    if (!logits || !topk_idx || !gates || !out) return MOE_EINVAL;
+    if (e_local > 0 && (!x || !w_gate || !w_up || !w_down)) return MOE_EINVAL;
+    if (misaligned(logits) || misaligned(x) || misaligned(w_gate) || misaligned(w_up) || misaligned(w_down) ||
+        misaligned(residual) || misaligned(topk_idx) || misaligned(gates) || misaligned(out) || misaligned(ws))
+        return MOE_EALIGN;
+    const FewSizes z = few_sizes(T, K, e_local, H, F);
+    if (!ws || ws_bytes < z.total) return MOE_EWORKSPACE;
+    char* b = (char*)ws;
+    FewParams p{};
+    p.logits = logits;
+    p.x = x;
+    p.T = T;
+    p.E = E;
+    p.K = K;
+    p.e_begin = e_begin;
+    p.e_local = e_local;
+    p.w_gate = w_gate;
+    p.w_up = w_up;
+    p.w_down = w_down;
+    p.H = H;
+    p.F = F;
+    p.residual = residual;
+    p.topk_idx = topk_idx;
+    p.gates = gates;
+    p.out = out;
+    p.n_active = (int*)b;
+    p.arrived = (int*)(b + z.arrived);
+    p.active = (FewExpert*)(b + z.active);
+    p.pos = (int*)(b + z.pos);
+    p.h = (uint16_t*)(b + z.h);
+    p.y = (float*)(b + z.y);
+    hipStream_t s = (hipStream_t)stream;
+    // the weights that the tokens can touch would fill half of the last-level cache (256 MB) or more
+    const bool ntl = (int64_t)std::min(e_local, T * K) * 6 * H * F >= (128ll << 20);
+    if (T <= 16) return launch_few<1, 3>(p, ntl, s);
+    if (T <= 32) return launch_few<2, 2>(p, ntl, s);
+    return launch_few<4, 2>(p, ntl, s);
+}

@@ -51,6 +51,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "linear.hpp"
 #include "moe_common.hpp"
 #include "mx.hpp"
 
@@ -82,7 +83,8 @@ enum : int {
     EPI_SWIGLU_BWD = 2,
     EPI_F32 = 3,
     EPI_SWIGLU8 = 4,
-    EPI_SWIGLU_BWD8 = 5
+    EPI_SWIGLU_BWD8 = 5,
+    EPI_LINEAR = 6  // dense rows: bias, activation and residual (linear.hpp)
 };
 constexpr bool is_up(int epi) { return epi == EPI_SWIGLU || epi == EPI_SWIGLU8; }
 enum : int { SCHED_ROWS = 0, SCHED_WGRAD = 1 };
@@ -128,6 +130,8 @@ struct GemmParams {
     int stagger_phases;
     int8_t* q8;           // SWIGLU8 (out), SWIGLU_BWD8 (in): saved [a | b] in 8 bits, [rows, 2N]
     uint8_t* s8;          // their scale bytes, [rows, 2N/32]
+    const uint16_t* res;  // LINEAR: residual [rows, N], or NULL (c2: the saved z, or NULL)
+    int act;              // LINEAR: moe_act
 };
 
 typedef __attribute__((ext_vector_type(4))) int i32x4;
@@ -1363,7 +1367,7 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
         }
 
         // ---- epilogue: lane holds row (l%32) and columns 8*j4 + 4*(l/32) + 0..3 ----
-        if constexpr (EPI == EPI_BF16 || EPI == EPI_F32) {
+        if constexpr (EPI == EPI_BF16 || EPI == EPI_F32 || EPI == EPI_LINEAR) {
             // Plain results go out through LDS so that every store writes whole
             // 128-byte row lines (stored straight from the MFMA layout, each
             // store touches 32 rows).  The stage slot of the last stage (gs-1)
@@ -1389,7 +1393,7 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
             // row-tiled fp32 output with a bias: the bias of this lane's
             // columns is loaded, and waited for once, before the tile's first
             // store (a load issued behind stores also waits for them)
-            constexpr bool kBias = EPI == EPI_F32 && SCHED == SCHED_ROWS;
+            constexpr bool kBias = (EPI == EPI_F32 || EPI == EPI_LINEAR) && SCHED == SCHED_ROWS;
             f32x4 bias_v[kBias ? NTW : 1] = {};
             if constexpr (kBias) {
                 if (p.bias) {
@@ -1404,8 +1408,28 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
             }
             constexpr int kRounds = NTW / kTilesPerRound;
             static_assert(kRounds % kBufs == 0, "rounds in whole pairs");
+            // LINEAR: the residual of a 32-row block, loaded before the block
+            // before it is stored (a load waits for the stores issued ahead of it)
+            u32x2 res_v[EPI == EPI_LINEAR ? 2 : 1][EPI == EPI_LINEAR ? NTW : 1][4] = {};
+            auto load_res = [&](int mt) {
+#pragma unroll
+                for (int np = 0; np < NTW; ++np)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int mloc = row_base(mt) + 8 * i + (ln >> 3);
+                        const int n = ni * BN + wn * (BN / WN) + 32 * np + 4 * (ln & 7);
+                        if (mloc < valid && n < p.N)
+                            res_v[mt & 1][np][i] = *(const u32x2*)(p.res + (int64_t)(row0 + mloc) * p.ldc + n);
+                    }
+            };
+            if constexpr (EPI == EPI_LINEAR) {
+                if (p.res) load_res(0);
+            }
 #pragma unroll
             for (int mt = 0; mt < MTW; ++mt) {
+                if constexpr (EPI == EPI_LINEAR) {
+                    if (p.res && mt + 1 < MTW) load_res(mt + 1);
+                }
                 // one row block after another (the scheduler does not interleave
                 // blocks); with the packed pair conversion below, the 256-row
                 // bodies of this epilogue do not spill
@@ -1451,6 +1475,16 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
                                 float* base = second ? p.cf2 : p.cf;
                                 const int nn = second ? n - p.n_split : n;
                                 *(u32x4*)(base + ((int64_t)j * p.M + m) * p.n_split + nn) = v;
+                            }
+                        } else if constexpr (EPI == EPI_LINEAR) {
+                            const int n = ni * BN + wn * (BN / WN) + 32 * np + 4 * c;
+                            if (mloc < valid && n < p.N) {
+                                const int64_t at = (int64_t)(row0 + mloc) * p.ldc + n;
+                                f32x4 f = __builtin_bit_cast(f32x4, v) + bias_v[np];
+                                if (p.c2) *(u32x2*)(p.c2 + at) = u32x2{pack_bf2x(f[0], f[1]), pack_bf2x(f[2], f[3])};
+                                activate(f, p.act);
+                                if (p.res) f += widen4(res_v[mt & 1][np][i]);
+                                *(u32x2*)(p.c + at) = u32x2{pack_bf2x(f[0], f[1]), pack_bf2x(f[2], f[3])};
                             }
                         } else {
                             // row-tiled fp32 output: one partial per contraction chunk
@@ -1848,7 +1882,7 @@ void gg_kernel(GemmParams p) {
     }
     __syncthreads();
     // the non-temporal weight path exists for the forward GEMMs (weights N-contiguous)
-    constexpr bool kNtPath = SCHED == SCHED_ROWS && LB == LAY_MN && EPI != EPI_F32;
+    constexpr bool kNtPath = SCHED == SCHED_ROWS && LB == LAY_MN && EPI != EPI_F32 && EPI != EPI_LINEAR;
     if constexpr (kNtPath) {
         for (int j = threadIdx.x; j < p.e_local; j += TL::kThreads) atomicMax(&s_maxrows, s_off[j + 1] - s_off[j]);
         __syncthreads();
@@ -1966,11 +2000,27 @@ inline bool fits_chip(const GemmParams& p, int bm, int cols, int per_cu = 2) {
     return (avg + bm - 1) / bm * p.e_local * ((p.N + cols - 1) / cols) <= per_cu * (int64_t)moe_host::num_cus();
 }
 
+inline size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+
+// Chunks of a contraction of kt_total steps so that `tiles` output tiles
+// become at most one workgroup per compute unit (a second, partial round of
+// workgroups would double the time), each chunk at least 8 steps.
+inline void split_steps(int64_t tiles, int64_t kt_total, int* n_chunks, int* steps) {
+    kt_total = std::max<int64_t>(kt_total, 1);  // no tokens: one (empty) chunk
+    const int64_t cus = moe_host::num_cus();
+    int64_t s = std::min<int64_t>(cus / std::max<int64_t>(tiles, 1), std::max<int64_t>(kt_total / 8, 1));
+    s = std::max<int64_t>(s, 1);
+    const int64_t st = (kt_total + s - 1) / s;
+    *steps = (int)st;
+    *n_chunks = (int)((kt_total + st - 1) / st);
+}
+
 // Launchers of the instantiations, each compiled in one translation unit
-// (gemm_rows.hip, gemm_dgrad.hip, gemm_wgrad.hip), so that no kernel is
-// instantiated twice in the library.
+// (gemm_rows.hip, gemm_dgrad.hip, gemm_wgrad.hip, gemm_router.hip), so that no
+// kernel is instantiated twice in the library.
 int launch_rows_mn(const GemmParams& p, int epi, hipStream_t s);  // B [Kd][N]; EPI_BF16 or EPI_SWIGLU_BWD
 int launch_rows_kc(const GemmParams& p, int epi, hipStream_t s);  // B [N][Kd]; EPI_BF16 or EPI_SWIGLU_BWD
 int launch_wgrad(const GemmParams& p, hipStream_t s);             // SCHED_WGRAD, fp32 out
+int launch_rows_f32_small(const GemmParams& p, hipStream_t s);    // B [Kd][N], fp32 out or partials, 128 x 128 tiles
 
 }  // namespace moe

@@ -6,17 +6,8 @@ using moe_host::misaligned;
 
 namespace moe {
 
-// Chunks of a contraction of kt_total steps so that `tiles` output tiles
-// become at most one workgroup per compute unit (a second, partial round of
-// workgroups would double the time), each chunk at least 8 steps.
-static void split_steps(int64_t tiles, int64_t kt_total, int* n_chunks, int* steps) {
-    kt_total = std::max<int64_t>(kt_total, 1);  // no tokens: one (empty) chunk
-    const int64_t cus = moe_host::num_cus();
-    int64_t s = std::min<int64_t>(cus / std::max<int64_t>(tiles, 1), std::max<int64_t>(kt_total / 8, 1));
-    s = std::max<int64_t>(s, 1);
-    const int64_t st = (kt_total + s - 1) / s;
-    *steps = (int)st;
-    *n_chunks = (int)((kt_total + st - 1) / st);
+int launch_rows_f32_small(const GemmParams& p, hipStream_t s) {
+    return launch_cfg<128, 128, 32, 2, 2, LAY_MN, EPI_F32, SCHED_ROWS, kLdsBudget>(p, s);
 }
 
 struct RouterPlan {
@@ -25,8 +16,6 @@ struct RouterPlan {
     int bwd_chunks, bwd_rows;     // weight gradient: token rows in chunks of bwd_rows
     size_t fwd_bytes, bwd_bytes;  // workspace
 };
-
-static size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 static RouterPlan router_plan(int T, int H, int E) {
     RouterPlan r{};
@@ -95,8 +84,7 @@ extern "C" int moe_router_logits(const moe_bf16* x, int T, int H, const moe_bf16
     p.part_stride = (int64_t)T * E;
     p.bias = split ? nullptr : bias;
     hipStream_t s = (hipStream_t)stream;
-    int rc = r.fwd_small ? launch_cfg<128, 128, 32, 2, 2, LAY_MN, EPI_F32, SCHED_ROWS, kLdsBudget>(p, s)
-                         : launch<LAY_MN, EPI_F32, SCHED_ROWS>(p, s);
+    int rc = r.fwd_small ? launch_rows_f32_small(p, s) : launch<LAY_MN, EPI_F32, SCHED_ROWS>(p, s);
     if (rc != MOE_OK || !split) return rc;
     return moe_host::sum_partials((const float*)ws, r.fwd_chunks, (int64_t)T * E, (int64_t)T * E, bias, E, logits, s);
 }

@@ -48,7 +48,6 @@ __global__ __launch_bounds__(256) void sum_split_kernel(const f32x4* __restrict_
     }
 }
 
-static size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 }  // namespace moe
 

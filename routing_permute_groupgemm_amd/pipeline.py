@@ -180,6 +180,35 @@ def forward4(buf: MoeBuffers, inp: dict):
     return buf.out
 
 
+@dataclasses.dataclass
+class FewBuffers:
+    """Buffers of forward_few: a decode step of at most _lib.MOE_FEW_TOKENS tokens."""
+    shape: MoeShape
+    topk_idx: torch.Tensor
+    gates: torch.Tensor
+    out: torch.Tensor
+    ws: torch.Tensor
+
+    @classmethod
+    def allocate(cls, shape: MoeShape, device="cuda"):
+        T, K = shape.T, shape.K
+        if T > _lib.MOE_FEW_TOKENS:
+            raise _lib.MoeError(f"FewBuffers: at most {_lib.MOE_FEW_TOKENS} tokens, got {T}")
+        ws_bytes = max(_lib.moe_layer_few_workspace_size(T, K, shape.EL, shape.H, shape.F), 256)
+        e = lambda *s, dt: torch.empty(*s, dtype=dt, device=device)  # noqa: E731
+        return cls(shape=shape, topk_idx=e((T, K), dt=torch.int32), gates=e((T, K), dt=torch.float32),
+                   out=e((T, shape.H), dt=torch.bfloat16), ws=e(ws_bytes, dt=torch.uint8))
+
+
+def forward_few(buf: FewBuffers, inp: dict, residual: torch.Tensor | None = None):
+    """forward for a few tokens in two launches, from the same inputs (logits, x and the bf16 weights); residual
+    (bf16 [T, H], buf.out itself too) is added before the output's one rounding."""
+    s = buf.shape
+    _lib.moe_layer_few(inp["logits"], inp["x"], s.K, s.e_begin, inp["w_gate"], inp["w_up"], inp["w_down"],
+                       residual=residual, topk_idx=buf.topk_idx, gates=buf.gates, out=buf.out, ws=buf.ws)
+    return buf.out
+
+
 def backward(buf: MoeBuffers, inp: dict):
     """inp additionally holds d_out (and x, read by the zero-copy weight gradient). Needs the forward's
     ab_save, or its 8-bit (a, b), from which h is recomputed into buf.h (whatever it holds by then)."""
