@@ -159,6 +159,11 @@ __device__ __forceinline__ void route_few(const FewParams& p, FewPlan& s, bool w
     __syncthreads();
 }
 
+// Workgroup b runs on XCD b % 8, and each XCD takes a contiguous run of the column blocks (neighbouring blocks of an
+// expert read neighbouring pieces of the same matrix rows, and the same tokens): 475 against 492 us for 64 tokens on 32
+// of 256 experts.  (The down kernel did not gain from it.)
+__device__ __forceinline__ int xcd_order(int b, int run) { return (b & 7) * run + (b >> 3); }
+
 template <int MT, int S, int W, bool NTL>
 __global__ __launch_bounds__(64 * W) void few_up(FewParams p) {
     __shared__ FewPlan plan;
@@ -167,38 +172,59 @@ __global__ __launch_bounds__(64 * W) void few_up(FewParams p) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int slabs = p.F / kFewUpCols;
-    const int total = plan.n_active * slabs;
-    for (int id = blockIdx.x; id < total; id += gridDim.x) {
+    const int total = plan.n_active * slabs, run = (total + 7) / 8;
+    for (int b = blockIdx.x; b < 8 * run; b += gridDim.x) {
+        const int id = xcd_order(b, run);
+        if (id >= total) continue;
         const int a = id / slabs, col0 = (id - a * slabs) * kFewUpCols;
         const int j = __builtin_amdgcn_readfirstlane((int)plan.expert[a]);
-        const int row0 = __builtin_amdgcn_readfirstlane((int)plan.row0[a]);
-        const int rows = __builtin_amdgcn_readfirstlane(__popcll(plan.mask[j]));
-        uint32_t x_at[MT];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-            x_at[m] = (uint32_t)plan.token[row0 + min(16 * m + (lane & 15), rows - 1)] * (uint32_t)(p.H * 2);
         const int64_t at = (int64_t)j * p.H * p.F;
         const uint16_t* const w[2] = {p.w_gate + at, p.w_up + at};
-        RowStream<2, 4, MT, S, NTL> r;
-        r.run(w, p.F, col0 + 4 * (lane & 15), p.x, x_at, rows, wave, W, p.H / 32);
+        const int end = __builtin_amdgcn_readfirstlane((int)plan.row0[a] + __popcll(plan.mask[j]));
+        for (int row0 = __builtin_amdgcn_readfirstlane((int)plan.row0[a]); row0 < end; row0 += 16 * MT) {
+            const int rows = min(16 * MT, end - row0);
+            uint32_t x_at[MT];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            if (16 * m >= rows) break;
-            __syncthreads();  // the sums of the block before are read
-            sums.put(r, m, wave, lane);
-            __syncthreads();
-            for (int i = tid; i < 256; i += 64 * W) {
-                const int row = i >> 4, c = (i & 15) * 4;
-                if (16 * m + row >= rows) continue;
-                const f32x4 g = sums.get(row, c), u = sums.get(row, 64 + c);
-                float v[4];
+            for (int m = 0; m < MT; ++m)
+                x_at[m] = (uint32_t)plan.token[row0 + min(16 * m + (lane & 15), rows - 1)] * (uint32_t)(p.H * 2);
+            RowStream<2, 4, MT, S, NTL> r;
+            r.run(w, p.F, col0 + 4 * (lane & 15), p.x, x_at, rows, wave, W, p.H / 32);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = silu_f(g[e]) * u[e];
-                *(u32x2*)(p.h + (int64_t)(row0 + 16 * m + row) * p.F + col0 + c) =
-                    u32x2{pack_bf2x(v[0], v[1]), pack_bf2x(v[2], v[3])};
+            for (int m = 0; m < MT; ++m) {
+                if (16 * m >= rows) break;
+                __syncthreads();  // the sums of the block before are read
+                sums.put(r, m, wave, lane);
+                __syncthreads();
+                for (int i = tid; i < 256; i += 64 * W) {
+                    const int row = i >> 4, c = (i & 15) * 4;
+                    if (16 * m + row >= rows) continue;
+                    const f32x4 g = sums.get(row, c), u = sums.get(row, 64 + c);
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = silu_f(g[e]) * u[e];
+                    *(u32x2*)(p.h + (int64_t)(row0 + 16 * m + row) * p.F + col0 + c) =
+                        u32x2{pack_bf2x(v[0], v[1]), pack_bf2x(v[2], v[3])};
+                }
             }
         }
     }
+}
+
+// fp32 rows that workgroups on other XCDs read within the same launch: accesses of the whole GPU's scope, which an
+// XCD's own L2 does not keep back.  Fences over it would write back and drop all of that L2 instead: with one a
+// workgroup the down kernel took 292 us for 23 tokens
+// (H = 2048, F = 768, 128 experts, top 8), and 64 without.
+__device__ __forceinline__ void store_shared(float* p, f32x4 v) {
+    const u32x4 u = __builtin_bit_cast(u32x4, v);
+    unsigned long long* q = (unsigned long long*)p;
+    __hip_atomic_store(q, (unsigned long long)u[1] << 32 | u[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(q + 1, (unsigned long long)u[3] << 32 | u[2], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x4 load_shared(const float* p) {
+    unsigned long long* q = (unsigned long long*)p;
+    const unsigned long long a = __hip_atomic_load(q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const unsigned long long b = __hip_atomic_load(q + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return __builtin_bit_cast(f32x4, u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)});
 }
 
 // The gated sums of columns col0 .. col0+127 of every token.
@@ -212,7 +238,7 @@ __device__ __forceinline__ void combine_few(const FewParams& p, int col0) {
         f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int k = 0; k < p.K; ++k) {
             const int r = p.pos[t * p.K + k];
-            if (r >= 0) acc += p.gates[t * p.K + k] * *(const f32x4*)(p.y + (int64_t)r * p.H + n);
+            if (r >= 0) acc += p.gates[t * p.K + k] * load_shared(p.y + (int64_t)r * p.H + n);
         }
         if (p.residual) {
             const u32x2 v = *(const u32x2*)(p.residual + (int64_t)t * p.H + n);
@@ -230,43 +256,46 @@ __global__ __launch_bounds__(64 * W) void few_down(FewParams p) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int slabs = (p.H + kFewDownCols - 1) / kFewDownCols;
     const int n_active = *p.n_active;
-    const int a = (int)blockIdx.x / slabs, slab = (int)blockIdx.x % slabs, col0 = slab * kFewDownCols;
+    const int a = (int)blockIdx.x / slabs, slab = (int)blockIdx.x - a * slabs, col0 = slab * kFewDownCols;
     if (a >= n_active) {
         // no pair is local: the sums are empty
         if (n_active == 0 && a == 0) combine_few<W>(p, col0);
         return;
     }
     const FewExpert e = p.active[a];
-    const int j = __builtin_amdgcn_readfirstlane(e.j), row0 = __builtin_amdgcn_readfirstlane(e.row0);
-    const int rows = __builtin_amdgcn_readfirstlane(e.rows);
-    uint32_t x_at[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) x_at[m] = (uint32_t)(row0 + min(16 * m + (lane & 15), rows - 1)) * (uint32_t)(p.F * 2);
+    const int j = __builtin_amdgcn_readfirstlane(e.j);
+    const int end = __builtin_amdgcn_readfirstlane(e.row0 + e.rows);
     const uint16_t* const w[1] = {p.w_down + (int64_t)j * p.F * p.H};
-    RowStream<1, 8, MT, S, NTL> r;
-    // columns past the last are read as the last ones; their sums are not stored
-    r.run(w, p.H, min(col0 + 8 * (lane & 15), p.H - 8), p.h, x_at, rows, wave, W, p.F / 32);
+    for (int row0 = __builtin_amdgcn_readfirstlane(e.row0); row0 < end; row0 += 16 * MT) {
+        const int rows = min(16 * MT, end - row0);
+        uint32_t x_at[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        if (16 * m >= rows) break;
-        if (m > 0) __syncthreads();
-        sums.put(r, m, wave, lane);
-        __syncthreads();
-        for (int i = tid; i < 512; i += 64 * W) {
-            const int row = i >> 5, c = (i & 31) * 4;
-            if (16 * m + row < rows && col0 + c < p.H)
-                *(f32x4*)(p.y + (int64_t)(row0 + 16 * m + row) * p.H + col0 + c) = sums.get(row, c);
+        for (int m = 0; m < MT; ++m)
+            x_at[m] = (uint32_t)(row0 + min(16 * m + (lane & 15), rows - 1)) * (uint32_t)(p.F * 2);
+        RowStream<1, 8, MT, S, NTL> r;
+        // columns past the last are read as the last ones; their sums are not stored
+        r.run(w, p.H, min(col0 + 8 * (lane & 15), p.H - 8), p.h, x_at, rows, wave, W, p.F / 32);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            if (16 * m >= rows) break;
+            __syncthreads();  // the sums of the block before are read
+            sums.put(r, m, wave, lane);
+            __syncthreads();
+            for (int i = tid; i < 512; i += 64 * W) {
+                const int row = i >> 5, c = (i & 31) * 4;
+                if (16 * m + row < rows && col0 + c < p.H)
+                    store_shared(p.y + (int64_t)(row0 + 16 * m + row) * p.H + col0 + c, sums.get(row, c));
+            }
         }
     }
-    // The last of the column block's workgroups sees every other's rows: each makes its own visible to the whole
-    // GPU before it counts itself, and the last one reads after it has seen the full count.
-    __threadfence();
+    // The last of the column block's workgroups to count itself finds every other's rows in memory: a wave's stores
+    // have arrived there when its count of outstanding ones is 0, all waves have when the barrier is passed, and only
+    // then does the workgroup count itself.  The last one's loads are issued after it has the full count.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (tid == 0) s_last = atomicAdd(p.arrived + slab, 1) == n_active - 1;
+    if (tid == 0) s_last = __hip_atomic_fetch_add(p.arrived + slab, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == n_active - 1;
     __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    combine_few<W>(p, col0);
+    if (s_last) combine_few<W>(p, col0);
 }
 
 struct FewSizes {
@@ -295,11 +324,13 @@ static int few_check(int T, int E, int K, int e_local, int H, int F) {
     return MOE_OK;
 }
 
-template <int MT, int S>
-static int launch_few(const FewParams& p, bool ntl, hipStream_t s) {
-    constexpr int W = 4;
+template <int MT, int S, int W>
+static int launch_few(const FewParams& p, hipStream_t s) {
     const int experts = std::min(p.e_local, p.T * p.K);
-    const int64_t up = std::max<int64_t>(1, std::min<int64_t>((int64_t)experts * (p.F / kFewUpCols), 3 * moe_host::num_cus()));
+    // the weights that the tokens can touch would fill half of the last-level cache (256 MB) or more
+    const bool ntl = (int64_t)experts * 6 * p.H * p.F >= (128ll << 20);
+    const int64_t up = std::max<int64_t>(
+        1, std::min<int64_t>((int64_t)experts * (p.F / kFewUpCols), 16 / W * moe_host::num_cus()));
     const int64_t down = (int64_t)std::max(experts, 1) * ((p.H + kFewDownCols - 1) / kFewDownCols);
     if (ntl) few_up<MT, S, W, true><<<(unsigned)up, 64 * W, 0, s>>>(p);
     else few_up<MT, S, W, false><<<(unsigned)up, 64 * W, 0, s>>>(p);
@@ -308,6 +339,25 @@ static int launch_few(const FewParams& p, bool ntl, hipStream_t s) {
     if (ntl) few_down<MT, S, W, true><<<(unsigned)down, 64 * W, 0, s>>>(p);
     else few_down<MT, S, W, false><<<(unsigned)down, 64 * W, 0, s>>>(p);
     return moe_host::launch_status();
+}
+
+// Row tiles a pass over an expert's weights (MT), stages (S) and waves a workgroup (W), from the sizes; the numbers are us
+// a call (H = 4096, F = 1536, E = 128, K = 8 if nothing else is said).
+//   MT  one tile of 16 rows: an expert with more takes another pass over its weights, which is rare while T*K/E, the
+//       rows that it has on average, are few (64 tokens on 32 of 256 experts, H = 7168, F = 2048: 487, and 589 with four
+//       tiles, whose sums cost the registers of loads in flight).  From 16 on, as many tiles as T can need (64 tokens on
+//       all of 8 experts: 145 with four, 278 with one).
+//   W   4; 8 where the routing (each wave takes T/W tokens) or the rows' loads count, from T > 32 or 8 rows an expert
+//       (64 tokens of the former: 487 against 524; 16 on all of 8 experts: 75 against 80; but one token 69.2 against 67.8).
+//   S   3 where gate and up have at most one workgroup a CU (one token: 67.8, and 70.6 with 2), or with W = 8 and one
+//       tile (487 against 497); else 2 (8 tokens of the former: 170 against 176, 4 tokens 200 against 205).
+static int launch_few_rows(const FewParams& p, hipStream_t s) {
+    const int rows = p.T * p.K / p.E;
+    if (rows >= 16 && p.T > 32) return launch_few<4, 2, 8>(p, s);
+    if (rows >= 16 && p.T > 16) return launch_few<2, 2, 8>(p, s);
+    if (rows >= 8 || p.T > 32) return launch_few<1, 3, 8>(p, s);
+    if ((int64_t)std::min(p.e_local, p.T * p.K) * (p.F / kFewUpCols) <= moe_host::num_cus()) return launch_few<1, 3, 4>(p, s);
+    return launch_few<1, 2, 4>(p, s);
 }
 
 }  // namespace moe
@@ -358,10 +408,5 @@ extern "C" int moe_layer_few(const float* logits, const moe_bf16* x, int T, int 
     p.pos = (int*)(b + z.pos);
     p.h = (uint16_t*)(b + z.h);
     p.y = (float*)(b + z.y);
-    hipStream_t s = (hipStream_t)stream;
-    // the weights that the tokens can touch would fill half of the last-level cache (256 MB) or more
-    const bool ntl = (int64_t)std::min(e_local, T * K) * 6 * H * F >= (128ll << 20);
-    if (T <= 16) return launch_few<1, 3>(p, ntl, s);
-    if (T <= 32) return launch_few<2, 2>(p, ntl, s);
-    return launch_few<4, 2>(p, ntl, s);
+    return launch_few_rows(p, (hipStream_t)stream);
 }
