@@ -1367,7 +1367,86 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
         }
 
         // ---- epilogue: lane holds row (l%32) and columns 8*j4 + 4*(l/32) + 0..3 ----
-        if constexpr (EPI == EPI_BF16 || EPI == EPI_F32 || EPI == EPI_LINEAR) {
+        if constexpr (EPI == EPI_LINEAR) {
+            // Lane l holds row l%32 and columns 8*j4 + 4*(l/32) + 0..3 of a 32 x 32 block.  A swap between the wave's
+            // halves turns two such groups of packed results into 8 neighbouring columns of a row, 16 bytes a lane and 32
+            // bytes of a row an instruction (which the cache merges into lines), and the residual's 16 bytes into the
+            // groups that the sums have: no staging through LDS.  The residual of the whole tile is asked for before the
+            // first store, so that no load waits for a store.
+            const int ln = lane_id_here();
+            const int h = ln >> 5;
+            auto swap_halves = [](uint32_t& a, uint32_t& b) {  // a's upper half of lanes with b's lower half
+                const auto s = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+                a = s[0];
+                b = s[1];
+            };
+            auto packed = [&](const f32x4& lo, const f32x4& hi) {
+                u32x4 v = {pack_bf2x(lo[0], lo[1]), pack_bf2x(lo[2], lo[3]), pack_bf2x(hi[0], hi[1]), pack_bf2x(hi[2], hi[3])};
+                uint32_t a0 = v[0], a1 = v[1], b0 = v[2], b1 = v[3];
+                swap_halves(a0, b0);
+                swap_halves(a1, b1);
+                return u32x4{a0, a1, b0, b1};
+            };
+            u32x4 res[MTW][NTW][2] = {};
+            if (p.res) {
+#pragma unroll
+                for (int mt = 0; mt < MTW; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < NTW; ++nt)
+#pragma unroll
+                        for (int jp = 0; jp < 2; ++jp) {
+                            const int mloc = row_base(mt) + (ln & 31), n = ni * BN + col_of(nt) + 16 * jp + 8 * h;
+                            if (mloc < valid && n < p.N)
+                                res[mt][nt][jp] = *(const u32x4*)(p.res + (int64_t)(row0 + mloc) * p.ldc + n);
+                        }
+            }
+            // the wave's bias columns wait in the stage slot that is free until the next stage issues its loads (in
+            // registers they would make the 256-row body spill)
+            static_assert(TL::kStage / TL::kWaves >= NTW * 128, "room for the bias");
+            uint8_t* stg = smem + ((gs + S - 1) % S) * TL::kStage + wave * (NTW * 128);
+            if (ln < NTW * 8) {
+                const int n = ni * BN + col_of(0) + 4 * ln;
+                *(MOE_LDS f32x4*)(stg + 16 * ln) = p.bias && n < p.N ? *(const f32x4*)(p.bias + n) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+#pragma unroll
+            for (int mt = 0; mt < MTW; ++mt) {
+                __builtin_amdgcn_sched_barrier(0);
+                const int mloc = row_base(mt) + (ln & 31);
+#pragma unroll
+                for (int nt = 0; nt < NTW; ++nt)
+#pragma unroll
+                    for (int jp = 0; jp < 2; ++jp) {
+                        const f32x16& a = acc[mt][nt];
+                        f32x4 f[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            f[e] = f32x4{a[8 * jp + 4 * e], a[8 * jp + 4 * e + 1], a[8 * jp + 4 * e + 2], a[8 * jp + 4 * e + 3]} +
+                                   *(const MOE_LDS f32x4*)(stg + 128 * nt + 32 * (2 * jp + e) + 16 * h);
+                        const int n = ni * BN + col_of(nt) + 16 * jp + 8 * h;
+                        const bool in = mloc < valid && n < p.N;
+                        const int64_t at = (int64_t)(row0 + mloc) * p.ldc + n;
+                        if (p.c2) {
+                            const u32x4 z = packed(f[0], f[1]);
+                            if (in) *(u32x4*)(p.c2 + at) = z;
+                        }
+                        activate(f[0], p.act);
+                        activate(f[1], p.act);
+                        if (p.res) {
+                            uint32_t r0 = res[mt][nt][jp][0], r1 = res[mt][nt][jp][1], r2 = res[mt][nt][jp][2],
+                                     r3 = res[mt][nt][jp][3];
+                            swap_halves(r0, r2);
+                            swap_halves(r1, r3);
+                            f[0] += widen4(u32x2{r0, r1});
+                            f[1] += widen4(u32x2{r2, r3});
+                        }
+                        const u32x4 y = packed(f[0], f[1]);
+                        if (in) *(u32x4*)(p.c + at) = y;
+                    }
+            }
+            __syncthreads();  // every wave is done with the slot before the next stage refills it
+            continue;
+        }
+        if constexpr (EPI == EPI_BF16 || EPI == EPI_F32) {
             // Plain results go out through LDS so that every store writes whole
             // 128-byte row lines (stored straight from the MFMA layout, each
             // store touches 32 rows).  The stage slot of the last stage (gs-1)
@@ -1393,7 +1472,7 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
             // row-tiled fp32 output with a bias: the bias of this lane's
             // columns is loaded, and waited for once, before the tile's first
             // store (a load issued behind stores also waits for them)
-            constexpr bool kBias = (EPI == EPI_F32 || EPI == EPI_LINEAR) && SCHED == SCHED_ROWS;
+            constexpr bool kBias = EPI == EPI_F32 && SCHED == SCHED_ROWS;
             f32x4 bias_v[kBias ? NTW : 1] = {};
             if constexpr (kBias) {
                 if (p.bias) {
@@ -1408,28 +1487,8 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
             }
             constexpr int kRounds = NTW / kTilesPerRound;
             static_assert(kRounds % kBufs == 0, "rounds in whole pairs");
-            // LINEAR: the residual of a 32-row block, loaded before the block
-            // before it is stored (a load waits for the stores issued ahead of it)
-            u32x2 res_v[EPI == EPI_LINEAR ? 2 : 1][EPI == EPI_LINEAR ? NTW : 1][4] = {};
-            auto load_res = [&](int mt) {
-#pragma unroll
-                for (int np = 0; np < NTW; ++np)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int mloc = row_base(mt) + 8 * i + (ln >> 3);
-                        const int n = ni * BN + wn * (BN / WN) + 32 * np + 4 * (ln & 7);
-                        if (mloc < valid && n < p.N)
-                            res_v[mt & 1][np][i] = *(const u32x2*)(p.res + (int64_t)(row0 + mloc) * p.ldc + n);
-                    }
-            };
-            if constexpr (EPI == EPI_LINEAR) {
-                if (p.res) load_res(0);
-            }
 #pragma unroll
             for (int mt = 0; mt < MTW; ++mt) {
-                if constexpr (EPI == EPI_LINEAR) {
-                    if (p.res && mt + 1 < MTW) load_res(mt + 1);
-                }
                 // one row block after another (the scheduler does not interleave
                 // blocks); with the packed pair conversion below, the 256-row
                 // bodies of this epilogue do not spill
@@ -1475,16 +1534,6 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
                                 float* base = second ? p.cf2 : p.cf;
                                 const int nn = second ? n - p.n_split : n;
                                 *(u32x4*)(base + ((int64_t)j * p.M + m) * p.n_split + nn) = v;
-                            }
-                        } else if constexpr (EPI == EPI_LINEAR) {
-                            const int n = ni * BN + wn * (BN / WN) + 32 * np + 4 * c;
-                            if (mloc < valid && n < p.N) {
-                                const int64_t at = (int64_t)(row0 + mloc) * p.ldc + n;
-                                f32x4 f = __builtin_bit_cast(f32x4, v) + bias_v[np];
-                                if (p.c2) *(u32x2*)(p.c2 + at) = u32x2{pack_bf2x(f[0], f[1]), pack_bf2x(f[2], f[3])};
-                                activate(f, p.act);
-                                if (p.res) f += widen4(res_v[mt & 1][np][i]);
-                                *(u32x2*)(p.c + at) = u32x2{pack_bf2x(f[0], f[1]), pack_bf2x(f[2], f[3])};
                             }
                         } else {
                             // row-tiled fp32 output: one partial per contraction chunk
@@ -2020,7 +2069,9 @@ inline void split_steps(int64_t tiles, int64_t kt_total, int* n_chunks, int* ste
 // kernel is instantiated twice in the library.
 int launch_rows_mn(const GemmParams& p, int epi, hipStream_t s);  // B [Kd][N]; EPI_BF16 or EPI_SWIGLU_BWD
 int launch_rows_kc(const GemmParams& p, int epi, hipStream_t s);  // B [N][Kd]; EPI_BF16 or EPI_SWIGLU_BWD
+int launch_rows_kc_small(const GemmParams& p, hipStream_t s);     // the same with EPI_BF16 in 128 x 128 tiles
 int launch_wgrad(const GemmParams& p, hipStream_t s);             // SCHED_WGRAD, fp32 out
+int launch_wgrad_small(const GemmParams& p, hipStream_t s);       // the same in 128 x 128 tiles
 int launch_rows_f32_small(const GemmParams& p, hipStream_t s);    // B [Kd][N], fp32 out or partials, 128 x 128 tiles
 
 }  // namespace moe

@@ -16,6 +16,9 @@ using moe_host::misaligned;
 namespace moe {
 
 int launch_wgrad(const GemmParams& p, hipStream_t s) { return launch<LAY_MN, EPI_F32, SCHED_WGRAD>(p, s); }
+int launch_wgrad_small(const GemmParams& p, hipStream_t s) {
+    return launch_cfg<128, 128, 32, 2, 2, LAY_MN, EPI_F32, SCHED_WGRAD, kLdsBudget>(p, s);
+}
 static int launch_wgrad_gather(const GemmParams& p, hipStream_t s) {
     return launch<LAY_MN, EPI_F32, SCHED_WGRAD, true>(p, s);
 }

@@ -5,11 +5,11 @@
 //   z = x . w + bias (fp32),  y = bf16(act(z) + residual),  optionally bf16(z) for the backward
 //   dz = bf16(dy * act'(z)),  dx = bf16(dz . w^T),  dw = x^T . dz (fp32),  db = sum over rows of dy * act'(z) (fp32)
 //
-// Forward, by the number of rows:
-//   few rows (at most kFewRows)  the weights' bytes are the time: linear_rows streams them (rows_stream.hpp), the
-//     contraction in chunks over the workgroups where the columns alone are too few;
-//   more rows  the GroupGEMM's kernel on one dense group with EPI_LINEAR, or, where its tiles would leave most of the
-//     chip idle, 128 x 128 tiles over chunks of the contraction.
+// Forward, by the sizes (linear_plan):
+//   few rows   the weights' bytes are the time: linear_rows streams them (rows_stream.hpp), the contraction in chunks
+//              over the workgroups where the columns alone are too few;
+//   more rows  the GroupGEMM's kernel on one dense group with EPI_LINEAR, in 256 x 256 or 128 x 128 tiles, or 128 x 128
+//              tiles over chunks of the contraction where the tiles alone would leave most of the chip idle.
 // Chunks leave fp32 partial sums, which linear_finish adds in chunk order before it does what the epilogue does.
 // The backward's products are the GroupGEMM's as well; linear_slope forms dz and the partial column sums of db in
 // one pass.
@@ -20,9 +20,6 @@
 using moe_host::misaligned;
 
 namespace moe {
-
-constexpr int kFewRows = 64;
-constexpr int kRowsCols = 128;  // columns of a linear_rows workgroup
 
 struct LinearParams {
     const uint16_t* x;
@@ -46,33 +43,36 @@ __device__ __forceinline__ void finish4(const LinearParams& p, int64_t t, int n,
     *(u32x2*)(p.y + at) = u32x2{pack_bf2x(f[0], f[1]), pack_bf2x(f[2], f[3])};
 }
 
-template <int MT, int S, int W>
+// Blocks of 16*MT rows (blockIdx.y), 16*CW columns and contraction chunks.
+template <int CW, int MT, int S, int W>
 __global__ __launch_bounds__(64 * W) void linear_rows(LinearParams p) {
-    __shared__ __attribute__((aligned(16))) WaveSums<1, 8, W> sums;
+    constexpr int kCols = 16 * CW, kQuads = kCols / 4;
+    __shared__ __attribute__((aligned(16))) WaveSums<1, CW, W> sums;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int slabs = (p.N + kRowsCols - 1) / kRowsCols;
-    const int chunk = (int)blockIdx.x / slabs, col0 = ((int)blockIdx.x % slabs) * kRowsCols;
+    const int slabs = (p.N + kCols - 1) / kCols;
+    const int chunk = (int)blockIdx.x / slabs, col0 = ((int)blockIdx.x % slabs) * kCols;
+    const int row0 = (int)blockIdx.y * 16 * MT, rows = min(16 * MT, p.T - row0);
     uint32_t x_at[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) x_at[m] = (uint32_t)min(16 * m + (lane & 15), p.T - 1) * (uint32_t)(p.Kd * 2);
+    for (int m = 0; m < MT; ++m) x_at[m] = (uint32_t)min(16 * m + (lane & 15), rows - 1) * (uint32_t)(p.Kd * 2);
     const uint16_t* const w[1] = {p.w};
-    RowStream<1, 8, MT, S, false> r;
+    RowStream<1, CW, MT, S, false> r;
     // columns past the last are read as the last ones; their sums are not stored
-    r.run(w, p.N, min(col0 + 8 * (lane & 15), p.N - 8), p.x, x_at, p.T, chunk * p.steps + wave, W,
-          min((chunk + 1) * p.steps, p.Kd / 32));
+    r.run(w, p.N, min(col0 + CW * (lane & 15), p.N - CW), p.x + (int64_t)row0 * p.Kd, x_at, rows, chunk * p.steps + wave,
+          W, min((chunk + 1) * p.steps, p.Kd / 32));
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-        if (16 * m >= p.T) break;
+        if (16 * m >= rows) break;
         if (m > 0) __syncthreads();
         sums.put(r, m, wave, lane);
         __syncthreads();
-        for (int i = tid; i < 512; i += 64 * W) {
-            const int row = 16 * m + (i >> 5), c = (i & 31) * 4;
-            if (row >= p.T || col0 + c >= p.N) continue;
-            const f32x4 f = sums.get(i >> 5, c);
-            if (p.part) *(f32x4*)(p.part + ((int64_t)chunk * p.T + row) * p.N + col0 + c) = f;
-            else finish4(p, row, col0 + c, f);
+        for (int i = tid; i < 16 * kQuads; i += 64 * W) {
+            const int row = 16 * m + i / kQuads, c = (i % kQuads) * 4;
+            if (row >= rows || col0 + c >= p.N) continue;
+            const f32x4 f = sums.get(i / kQuads, c);
+            if (p.part) *(f32x4*)(p.part + ((int64_t)chunk * p.T + row0 + row) * p.N + col0 + c) = f;
+            else finish4(p, row0 + row, col0 + c, f);
         }
     }
 }
@@ -82,6 +82,7 @@ __global__ __launch_bounds__(256) void linear_finish(LinearParams p, int chunks)
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
         const f32x4* at = (const f32x4*)p.part + i;
         f32x4 f = *at;
+#pragma unroll 4
         for (int c = 1; c < chunks; ++c) f += at[c * stride];
         const int64_t t = i * 4 / p.N;
         finish4(p, t, (int)(i * 4 - t * p.N), f);
@@ -131,42 +132,101 @@ __global__ __launch_bounds__(256) void linear_slope(const uint16_t* dy, const ui
     }
 }
 
+// What a product on the GroupGEMM kernel takes, in us, fitted to what it was measured to take on the MI355X (both tile
+// sizes and every number of chunks, 256 to 65536 rows by 256 to 8192 columns and contraction values: the form that these
+// choose was the fastest or within 10% of it).  A 256 x 256 tile has a CU to itself, of 128 x 128 tiles a CU takes two; a
+// step is 32 contraction values, `step` and `fixed` a step's and a tile's share.
+static double big_tiles_us(int64_t n, int64_t steps, double step, double fixed) {
+    const int64_t cus = moe_host::num_cus();
+    return (double)((n + cus - 1) / cus) * (step * (double)steps + fixed);
+}
+static double small_tiles_us(int64_t n, int64_t steps, double alone, double shared) {
+    const int64_t cus = moe_host::num_cus();
+    return n <= cus ? alone * (double)steps + 4.0
+                    : (double)((n + 2 * cus - 1) / (2 * cus)) * (shared * (double)steps + 8.0);
+}
+// Partial sums of chunks (fp32), written and read, and the launch that adds them.
+static double partials_us(int64_t chunks, int64_t values) {
+    return chunks > 1 ? 2.0 + (double)(chunks * values) * 8.0 / 7e6 : 0.0;
+}
+
+static int64_t tiles_of(int64_t rows, int64_t cols, int edge) {
+    return ((rows + edge - 1) / edge) * ((cols + edge - 1) / edge);
+}
+
 enum : int { FORM_ROWS = 0, FORM_SMALL = 1, FORM_BIG = 2 };
+constexpr int kFewRows = 256;
 
 struct LinearPlan {
     int form, chunks, steps;      // forward
+    bool wide;                    // FORM_ROWS: 128 columns a workgroup, not 64
     int slope_rows;               // row blocks of linear_slope, and so partial rows of db
-    int dw_chunks, dw_rows;       // weight gradient: row chunks
+    bool dw_small;                // weight gradient: 128 x 128 tiles, not 256 x 256
+    int dw_chunks, dw_rows;       // and its row chunks
     size_t forward_bytes, db_bytes, backward_bytes;
 };
+
+// Few rows, measured (us, one product): blocks of 64 columns and up to 64 rows, in chunks that fill the GPU once, of at
+// least 8 steps.  1 x 7168 x 2048 (rows, contraction, columns): 9.6 with 8 chunks, 19 without; but a chunk's sums pass
+// through memory, so products of few rows and a short contraction are not cut (1 x 2048 x 7168: 8.2, and 8.9 in two), nor
+// those that fill most of the GPU (128 x 2048 x 7168: 17.3, and 22.7 in two).  128 columns, whose workgroups read the rows
+// half as often, where the columns are many: 64 x 7168 x 7168 31 against 38; 128 x 4096 x 1536 15.6 against 13.7.
+// 512 x 4096 x 1536 takes 24 in rows and in tiles, 256 x 4096 x 1536 18 in rows and 22 in tiles.
+static void plan_rows(LinearPlan& r, int T, int kt, int N) {
+    const int64_t cus = moe_host::num_cus();
+    r.form = FORM_ROWS;
+    r.wide = T > 32 && N >= 4096;
+    const int cols = r.wide ? 128 : 64;
+    const int64_t blocks = (int64_t)((N + cols - 1) / cols) * ((T + 63) / 64);
+    int64_t want = 1;
+    if (!(T <= 16 && kt <= 64) && 5 * blocks < 4 * cus)
+        want = std::max<int64_t>(1, std::min<int64_t>(cus / blocks, kt / 8));
+    r.steps = (int)((kt + want - 1) / want);
+    r.chunks = (kt + r.steps - 1) / r.steps;
+}
 
 static LinearPlan linear_plan(int T, int Kd, int N) {
     LinearPlan r{};
     const int64_t cus = moe_host::num_cus();
     const int kt = Kd / 32;
-    r.chunks = 1;
-    r.steps = kt;
-    const int64_t big = (int64_t)((T + 255) / 256) * ((N + 255) / 256);
     if (T <= kFewRows) {
-        r.form = FORM_ROWS;
-        const int64_t slabs = (N + kRowsCols - 1) / kRowsCols;
-        const int64_t want = std::max<int64_t>(1, std::min<int64_t>(cus / slabs, kt / 8));
-        r.steps = (int)((kt + want - 1) / want);
-        r.chunks = (kt + r.steps - 1) / r.steps;
-    } else if (big >= cus) {
-        r.form = FORM_BIG;
+        plan_rows(r, T, kt, N);
     } else {
-        r.form = FORM_SMALL;
-        split_steps((int64_t)((T + 127) / 128) * ((N + 127) / 128), kt, &r.chunks, &r.steps);
+        r.form = FORM_BIG;
+        r.chunks = 1;
+        r.steps = kt;
+        double best = big_tiles_us(tiles_of(T, N, 256), kt, 0.82, 26.0);
+        for (int c = 1; c <= 16 && (c == 1 || kt / c >= 8); c *= 2) {
+            const int steps = (kt + c - 1) / c, chunks = (kt + steps - 1) / steps;
+            const double t = small_tiles_us(tiles_of(T, N, 128) * chunks, steps, 0.37, 0.56) + partials_us(chunks, (int64_t)T * N);
+            if (t < best) {
+                best = t;
+                r.form = FORM_SMALL;
+                r.chunks = chunks;
+                r.steps = steps;
+            }
+        }
     }
     r.forward_bytes = r.chunks > 1 ? (size_t)r.chunks * T * N * 4 : 0;
     const int64_t blocks = (N + 511) / 512;
     r.slope_rows = (int)std::max<int64_t>(1, std::min<int64_t>(((int64_t)T + 15) / 16, 4 * cus / blocks));
     r.db_bytes = round256((size_t)r.slope_rows * N * 4);
+    // the weight gradient: the rows are the contraction
+    const int64_t rt = std::max<int64_t>(1, ((int64_t)T + 31) / 32), out = (int64_t)Kd * N;
     int steps;
-    split_steps((int64_t)((Kd + 255) / 256) * ((N + 255) / 256), ((int64_t)T + 31) / 32, &r.dw_chunks, &steps);
+    split_steps(tiles_of(Kd, N, 256), rt, &r.dw_chunks, &steps);
+    double best = big_tiles_us(tiles_of(Kd, N, 256) * r.dw_chunks, steps, 0.8, 11.0) + partials_us(r.dw_chunks, out);
+    for (int c = 1; c <= 32 && (c == 1 || rt / c >= 8); c *= 2) {
+        const int st = (int)((rt + c - 1) / c), chunks = (int)((rt + st - 1) / st);
+        const double t = small_tiles_us(tiles_of(Kd, N, 128) * chunks, st, 0.45, 0.62) + partials_us(chunks, out);
+        if (t < best) {
+            best = t;
+            r.dw_small = true;
+            r.dw_chunks = chunks;
+            steps = st;
+        }
+    }
     r.dw_rows = steps * 32;
-    r.dw_chunks = std::max(1, (int)(((int64_t)T + r.dw_rows - 1) / r.dw_rows));
     r.backward_bytes = r.db_bytes + (r.dw_chunks > 1 ? (size_t)r.dw_chunks * Kd * N * 4 : 0);
     return r;
 }
@@ -181,11 +241,10 @@ static int linear_check(int T, int Kd, int N, int act) {
     return MOE_OK;
 }
 
-template <int MT, int S>
+template <int CW, int MT, int S, int W>
 static int launch_linear_rows(const LinearParams& p, int chunks, hipStream_t s) {
-    constexpr int W = 4;
-    const int grid = (p.N + kRowsCols - 1) / kRowsCols * chunks;
-    linear_rows<MT, S, W><<<grid, 64 * W, 0, s>>>(p);
+    const dim3 grid((p.N + 16 * CW - 1) / (16 * CW) * chunks, (p.T + 16 * MT - 1) / (16 * MT));
+    linear_rows<CW, MT, S, W><<<grid, 64 * W, 0, s>>>(p);
     return moe_host::launch_status();
 }
 
@@ -243,9 +302,10 @@ extern "C" int moe_linear(const moe_bf16* x, int T, int Kd, const moe_bf16* w, i
     LinearParams p{x, w, bias, residual, z, y, r.chunks > 1 ? (float*)ws : nullptr, T, Kd, N, act, r.steps};
     int rc;
     if (r.form != FORM_ROWS) rc = linear_gemm(p, r, s);
-    else if (T <= 16) rc = launch_linear_rows<1, 3>(p, r.chunks, s);
-    else if (T <= 32) rc = launch_linear_rows<2, 2>(p, r.chunks, s);
-    else rc = launch_linear_rows<4, 2>(p, r.chunks, s);
+    else if (r.wide) rc = launch_linear_rows<8, 4, 2, 4>(p, r.chunks, s);
+    else if (T <= 16) rc = launch_linear_rows<4, 1, 3, 8>(p, r.chunks, s);
+    else if (T <= 32) rc = launch_linear_rows<4, 2, 2, 8>(p, r.chunks, s);
+    else rc = launch_linear_rows<4, 4, 2, 8>(p, r.chunks, s);
     if (rc != MOE_OK || r.chunks == 1) return rc;
     const int64_t blocks = std::min<int64_t>(((int64_t)T * N / 4 + 255) / 256, (int64_t)moe_host::num_cus() * 8);
     linear_finish<<<(int)blocks, 256, 0, s>>>(p, r.chunks);
@@ -302,7 +362,9 @@ extern "C" int moe_linear_backward(const moe_bf16* dy, const moe_bf16* x, int T,
         p.Kd = N;
         p.c = dx;
         p.ldc = Kd;
-        rc = launch_rows_kc(p, EPI_BF16, s);
+        const bool small = small_tiles_us(tiles_of(T, Kd, 128), N / 32, 0.37, 0.56) <
+                           big_tiles_us(tiles_of(T, Kd, 256), N / 32, 0.82, 12.0);
+        rc = small ? launch_rows_kc_small(p, s) : launch_rows_kc(p, EPI_BF16, s);
         if (rc != MOE_OK) return rc;
     }
     if (!dw) return MOE_OK;
@@ -319,7 +381,7 @@ extern "C" int moe_linear_backward(const moe_bf16* dy, const moe_bf16* x, int T,
     q.N = N;
     q.cf = split ? dw_part : dw;
     q.n_split = N;
-    rc = launch_wgrad(q, s);
+    rc = r.dw_small ? launch_wgrad_small(q, s) : launch_wgrad(q, s);
     if (rc != MOE_OK || !split) return rc;
     return moe_host::sum_partials(dw_part, r.dw_chunks, (int64_t)Kd * N, (int64_t)Kd * N, nullptr, N, dw, s);
 }
