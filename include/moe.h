@@ -512,8 +512,8 @@ int moe_grouped_gemm4_combine(const moe_bf16* a, const uint8_t* q4, const uint8_
  *   ws: device workspace of at least moe_layer_few_workspace_size(T, K, e_local,
  *   H, F) bytes, which the call initialises itself; one for each of calls that
  *   may overlap (graphs that are replayed at once among them).
- * T <= MOE_FEW_TOKENS and e_begin + e_local <= E (MOE_EINVAL); other limits and
- * errors as moe_route and moe_grouped_gemm_swiglu.  Every weight of an expert
+ * T <= MOE_FEW_TOKENS, e_begin + e_local <= E, H and F <= 65536 (MOE_EINVAL); other
+ * limits and errors as moe_route and moe_grouped_gemm_swiglu.  Every weight of an expert
  * that has a token is read once, so it is the faster form while the tokens are
  * few; pipeline.forward takes any number of them.
  */
@@ -578,7 +578,7 @@ enum moe_act {
  *   ws: device workspace of at least moe_linear_workspace_size(T, Kd, N) bytes
  *   (may be NULL when that is 0), one for each of calls that may overlap.
  * Kd and N multiples of 64 (MOE_ESHAPE); Kd * N * 2 < 2^31, 256 rows of x and y
- * below 2 GiB, T <= 2^30 (MOE_EINVAL).  Where the columns are too few to fill
+ * below 2 GiB, T <= 2^30, T * max(Kd, N) < 2^40 (MOE_EINVAL).  Where the columns are too few to fill
  * the GPU the contraction is cut into chunks whose fp32 partials are added in
  * chunk order: the order of a sum goes by the sizes and the GPU's number of CUs.
  */

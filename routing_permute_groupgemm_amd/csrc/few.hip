@@ -320,7 +320,7 @@ static int few_check(int T, int E, int K, int e_local, int H, int F) {
         F <= 0)
         return MOE_EINVAL;
     if (K > E || H % 64 || F % 64) return MOE_ESHAPE;
-    if ((int64_t)H * F * 2 >= (1ll << 31) || H > (1 << 24) || F > (1 << 20)) return MOE_EINVAL;
+    if ((int64_t)H * F * 2 >= (1ll << 31) || H > 65536 || F > 65536) return MOE_EINVAL;
     return MOE_OK;
 }
 

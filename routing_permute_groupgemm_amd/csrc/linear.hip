@@ -234,9 +234,9 @@ static LinearPlan linear_plan(int T, int Kd, int N) {
 static int linear_check(int T, int Kd, int N, int act) {
     if (T < 0 || T > (1 << 30) || Kd <= 0 || N <= 0 || act < MOE_ACT_NONE || act > MOE_ACT_GELU) return MOE_EINVAL;
     if (Kd % 64 || N % 64) return MOE_ESHAPE;
-    // 256 rows of an operand and the weights stay below 2 GiB (32-bit load offsets)
+    // 256 rows of an operand and the weights stay below 2 GiB (32-bit load offsets), the tiles below 2^31
     if (Kd > (1 << 21) || N > (1 << 21) || (int64_t)256 * std::max(Kd, N) * 2 >= (1ll << 31) ||
-        (int64_t)Kd * N * 2 >= (1ll << 31))
+        (int64_t)Kd * N * 2 >= (1ll << 31) || (int64_t)T * std::max(Kd, N) >= (1ll << 40))
         return MOE_EINVAL;
     return MOE_OK;
 }

@@ -175,6 +175,34 @@ def test_no_tokens():
     assert dz.shape == (0, 192) and dx.shape == (0, 128) and (dw == 0).all() and (db == 0).all()
 
 
+def test_outputs_past_2_31_values():
+    """Whole numbers again, 2^31 outputs and more: rows at both ends and around the border, bit for bit."""
+    T, Kd, N = 520001, 64, 4160
+    x, w, dy1 = ints(1, T, Kd), ints(2, Kd, N), ints(3, N, top=1)
+    res = torch.zeros((T, N), dtype=BF, device="cuda")
+    border = (1 << 31) // N
+    probe = torch.tensor([0, 1, 255, 256, border - 1, border, border + 1, T - 2, T - 1], device="cuda")
+    res[probe] = ints(4, len(probe), N, top=60)
+    print(f"[linear] {T} x {Kd} x {N}", flush=True)
+    y, z = _lib.moe_linear(x, w, act="relu", residual=res, want_z=True)
+    want = x[probe].double() @ w.double()
+    assert torch.equal(z[probe], want.float().to(BF))
+    assert torch.equal(y[probe], (want.clamp(min=0) + res[probe].double()).float().to(BF))
+    del res
+    dy = y.copy_(dy1)  # the same gradient in every row
+    dz, dx, dw, db = _lib.moe_linear_backward(dy, x, w, act="relu", z=z, dz=dy)
+    d = dy1.double() * (want > 0)
+    assert torch.equal(dz[probe], d.to(BF))
+    assert torch.equal(dx[probe], (d @ w.double().t().contiguous()).float().to(BF))
+    sign = torch.zeros(N, dtype=torch.float64, device="cuda")
+    grad = torch.zeros((Kd, N), dtype=torch.float64, device="cuda")
+    for lo in range(0, T, 40000):
+        part = dy1.double() * (x[lo:lo + 40000].double() @ w.double() > 0)
+        sign += part.sum(0)
+        grad += x[lo:lo + 40000].double().t().contiguous() @ part
+    assert torch.equal(db.double(), sign) and torch.equal(dw.double(), grad)
+
+
 def test_workspace_of_the_caller_and_what_is_behind_it():
     x, w, dy = rand(1, 70, 1024, dtype=BF), rand(2, 1024, 128, dtype=BF), rand(3, 70, 128, dtype=BF)
     n = _lib.moe_linear_workspace_size(70, 1024, 128)
