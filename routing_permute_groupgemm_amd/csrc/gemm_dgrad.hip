@@ -10,7 +10,8 @@ int launch_rows_kc(const GemmParams& p, int epi, hipStream_t s) {
     return launch<LAY_KC, EPI_BF16, SCHED_ROWS>(p, s);
 }
 
-int launch_rows_kc_small(const GemmParams& p, hipStream_t s) {
+int launch_rows_kc_small(const GemmParams& p, bool deep, hipStream_t s) {
+    if (deep) return launch_cfg<128, 128, 32, 2, 2, LAY_KC, EPI_BF16, SCHED_ROWS, kDeepBudget>(p, s);
     return launch_cfg<128, 128, 32, 2, 2, LAY_KC, EPI_BF16, SCHED_ROWS, kLdsBudget>(p, s);
 }
 

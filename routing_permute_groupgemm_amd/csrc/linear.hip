@@ -135,14 +135,16 @@ __global__ __launch_bounds__(256) void linear_slope(const uint16_t* dy, const ui
 // What a product on the GroupGEMM kernel takes, in us, fitted to what it was measured to take on the MI355X (both tile
 // sizes and every number of chunks, 256 to 65536 rows by 256 to 8192 columns and contraction values: the form that these
 // choose was the fastest or within 10% of it).  A 256 x 256 tile has a CU to itself, of 128 x 128 tiles a CU takes two; a
-// step is 32 contraction values, `step` and `fixed` a step's and a tile's share.
+// step is 32 contraction values, `step` and `fixed` a step's and a tile's share.  Small tiles that have a CU to themselves
+// run with eight stages of loads (1000 x 1024 x 4096: 19.5 with eight, 24.8 with
+// four).
 static double big_tiles_us(int64_t n, int64_t steps, double step, double fixed) {
     const int64_t cus = moe_host::num_cus();
     return (double)((n + cus - 1) / cus) * (step * (double)steps + fixed);
 }
-static double small_tiles_us(int64_t n, int64_t steps, double alone, double shared) {
+static double small_tiles_us(int64_t n, int64_t steps, double alone, double fixed, double shared) {
     const int64_t cus = moe_host::num_cus();
-    return n <= cus ? alone * (double)steps + 4.0
+    return n <= cus ? alone * (double)steps + fixed
                     : (double)((n + 2 * cus - 1) / (2 * cus)) * (shared * (double)steps + 8.0);
 }
 // Partial sums of chunks (fp32), written and read, and the launch that adds them.
@@ -198,7 +200,9 @@ static LinearPlan linear_plan(int T, int Kd, int N) {
         double best = big_tiles_us(tiles_of(T, N, 256), kt, 0.82, 26.0);
         for (int c = 1; c <= 16 && (c == 1 || kt / c >= 8); c *= 2) {
             const int steps = (kt + c - 1) / c, chunks = (kt + steps - 1) / steps;
-            const double t = small_tiles_us(tiles_of(T, N, 128) * chunks, steps, 0.37, 0.56) + partials_us(chunks, (int64_t)T * N);
+            const int64_t n = tiles_of(T, N, 128) * chunks;
+            const double t = (chunks == 1 ? small_tiles_us(n, steps, 0.27, 8.0, 0.56) : small_tiles_us(n, steps, 0.37, 4.0, 0.56)) +
+                             partials_us(chunks, (int64_t)T * N);
             if (t < best) {
                 best = t;
                 r.form = FORM_SMALL;
@@ -218,7 +222,7 @@ static LinearPlan linear_plan(int T, int Kd, int N) {
     double best = big_tiles_us(tiles_of(Kd, N, 256) * r.dw_chunks, steps, 0.8, 11.0) + partials_us(r.dw_chunks, out);
     for (int c = 1; c <= 32 && (c == 1 || rt / c >= 8); c *= 2) {
         const int st = (int)((rt + c - 1) / c), chunks = (int)((rt + st - 1) / st);
-        const double t = small_tiles_us(tiles_of(Kd, N, 128) * chunks, st, 0.45, 0.62) + partials_us(chunks, out);
+        const double t = small_tiles_us(tiles_of(Kd, N, 128) * chunks, st, 0.45, 4.0, 0.62) + partials_us(chunks, out);
         if (t < best) {
             best = t;
             r.dw_small = true;
@@ -273,6 +277,8 @@ static int linear_gemm(const LinearParams& l, const LinearPlan& r, hipStream_t s
     p.bias = l.bias;
     p.res = l.res;
     p.act = l.act;
+    if (r.form == FORM_SMALL && tiles_of(l.T, l.N, 128) <= moe_host::num_cus())
+        return launch_cfg<128, 128, 32, 2, 2, LAY_MN, EPI_LINEAR, SCHED_ROWS, kDeepBudget>(p, s);
     if (r.form == FORM_SMALL) return launch_cfg<128, 128, 32, 2, 2, LAY_MN, EPI_LINEAR, SCHED_ROWS, kLdsBudget>(p, s);
     return launch_cfg<256, 256, 32, 2, 2, LAY_MN, EPI_LINEAR, SCHED_ROWS, kLdsBudget>(p, s);
 }
@@ -362,9 +368,9 @@ extern "C" int moe_linear_backward(const moe_bf16* dy, const moe_bf16* x, int T,
         p.Kd = N;
         p.c = dx;
         p.ldc = Kd;
-        const bool small = small_tiles_us(tiles_of(T, Kd, 128), N / 32, 0.37, 0.56) <
-                           big_tiles_us(tiles_of(T, Kd, 256), N / 32, 0.82, 12.0);
-        rc = small ? launch_rows_kc_small(p, s) : launch_rows_kc(p, EPI_BF16, s);
+        const int64_t n = tiles_of(T, Kd, 128);
+        const bool small = small_tiles_us(n, N / 32, 0.27, 8.0, 0.56) < big_tiles_us(tiles_of(T, Kd, 256), N / 32, 0.82, 12.0);
+        rc = small ? launch_rows_kc_small(p, n <= moe_host::num_cus(), s) : launch_rows_kc(p, EPI_BF16, s);
         if (rc != MOE_OK) return rc;
     }
     if (!dw) return MOE_OK;
