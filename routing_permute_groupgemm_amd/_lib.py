@@ -879,7 +879,7 @@ def moe_layer_few(logits, x, K, e_begin, w_gate, w_up, w_down, residual=None, to
     out = _out(out, (T, H), torch.bfloat16, "out", dev, stream)
     lib = load()
     ws, size = _ws(ws, lib.moe_layer_few_workspace_size(T, K, EL, H, F), dev, stream)
-    _check(lib.moe_layer_few(_ptr(logits), _ptr(x), T, E, K, e_begin, EL, _ptr(w_gate), _ptr(w_up), _ptr(w_down), H, F,
+    _check(lib.moe_layer_few(_ptr(logits), _ptr(x), T, E, K, int(e_begin), EL, _ptr(w_gate), _ptr(w_up), _ptr(w_down), H, F,
                              res, _ptr(topk_idx), _ptr(gates), _ptr(out), _ptr(ws), size, _handle(stream, dev)))
     return out, topk_idx, gates
 

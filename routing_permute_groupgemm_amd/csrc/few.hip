@@ -213,7 +213,7 @@ __global__ __launch_bounds__(64 * W) void few_up(FewParams p) {
 // fp32 rows that workgroups on other XCDs read within the same launch: accesses of the whole GPU's scope, which an
 // XCD's own L2 does not keep back.  Fences over it would write back and drop all of that L2 instead: with one a
 // workgroup the down kernel took 292 us for 23 tokens
-// (H = 2048, F = 768, 128 experts, top 8), and 64 without.
+// (H = 2048, F = 768, 128 experts, top 8), with one that a single thread issues 127, and 64 without.
 __device__ __forceinline__ void store_shared(float* p, f32x4 v) {
     const u32x4 u = __builtin_bit_cast(u32x4, v);
     unsigned long long* q = (unsigned long long*)p;

@@ -8,8 +8,8 @@
 // Forward, by the sizes (linear_plan):
 //   few rows   the weights' bytes are the time: linear_rows streams them (rows_stream.hpp), the contraction in chunks
 //              over the workgroups where the columns alone are too few;
-//   more rows  the GroupGEMM's kernel on one dense group with EPI_LINEAR, in 256 x 256 or 128 x 128 tiles, or 128 x 128
-//              tiles over chunks of the contraction where the tiles alone would leave most of the chip idle.
+//   more rows  the GroupGEMM's kernel on one dense group with EPI_LINEAR, in tiles of 256 x 256, 128 x 256 or 128 x 128, or
+//              128 x 128 tiles over chunks of the contraction where the tiles alone would leave most of the chip idle.
 // Chunks leave fp32 partial sums, which linear_finish adds in chunk order before it does what the epilogue does.
 // The backward's products are the GroupGEMM's as well; linear_slope forms dz and the partial column sums of db in
 // one pass.
@@ -132,31 +132,29 @@ __global__ __launch_bounds__(256) void linear_slope(const uint16_t* dy, const ui
     }
 }
 
-// What a product on the GroupGEMM kernel takes, in us, fitted to what it was measured to take on the MI355X (both tile
-// sizes and every number of chunks, 256 to 65536 rows by 256 to 8192 columns and contraction values: the form that these
-// choose was the fastest or within 10% of it).  A 256 x 256 tile has a CU to itself, of 128 x 128 tiles a CU takes two; a
-// step is 32 contraction values, `step` and `fixed` a step's and a tile's share.  Small tiles that have a CU to themselves
-// run with eight stages of loads (1000 x 1024 x 4096: 19.5 with eight, 24.8 with
-// four).
-static double big_tiles_us(int64_t n, int64_t steps, double step, double fixed) {
+// What a product on the GroupGEMM kernel takes, in us, fitted to what it was measured to take on the MI355X (every form
+// and number of chunks, 257 to 65536 rows by 256 to 8192 columns and contraction values: the form that these choose was
+// the fastest or within 10% of it).  A step is 32 contraction values, `step` and `fixed` a step's and a tile's share.
+// Tiles that have a CU to themselves (all but the 128 x 128 ones of four waves, of which a CU takes two):
+static double tiles_us(int64_t n, int64_t steps, double step, double fixed) {
     const int64_t cus = moe_host::num_cus();
     return (double)((n + cus - 1) / cus) * (step * (double)steps + fixed);
 }
-static double small_tiles_us(int64_t n, int64_t steps, double alone, double fixed, double shared) {
+static double shared_us(int64_t n, int64_t steps, double alone, double shared) {
     const int64_t cus = moe_host::num_cus();
-    return n <= cus ? alone * (double)steps + fixed
+    return n <= cus ? alone * (double)steps + 4.0
                     : (double)((n + 2 * cus - 1) / (2 * cus)) * (shared * (double)steps + 8.0);
 }
 // Partial sums of chunks (fp32), written and read, and the launch that adds them.
-static double partials_us(int64_t chunks, int64_t values) {
-    return chunks > 1 ? 2.0 + (double)(chunks * values) * 8.0 / 7e6 : 0.0;
+static double partials_us(int64_t chunks, int64_t values, double launch) {
+    return chunks > 1 ? launch + (double)(chunks * values) * 8.0 / 7e6 : 0.0;
 }
 
-static int64_t tiles_of(int64_t rows, int64_t cols, int edge) {
-    return ((rows + edge - 1) / edge) * ((cols + edge - 1) / edge);
+static int64_t tiles_of(int64_t rows, int64_t cols, int bm, int bn) {
+    return ((rows + bm - 1) / bm) * ((cols + bn - 1) / bn);
 }
 
-enum : int { FORM_ROWS = 0, FORM_SMALL = 1, FORM_BIG = 2 };
+enum : int { FORM_ROWS = 0, FORM_SMALL = 1, FORM_MID = 2, FORM_BIG = 3, FORM_CHUNKS = 4 };
 constexpr int kFewRows = 256;
 
 struct LinearPlan {
@@ -197,18 +195,20 @@ static LinearPlan linear_plan(int T, int Kd, int N) {
         r.form = FORM_BIG;
         r.chunks = 1;
         r.steps = kt;
-        double best = big_tiles_us(tiles_of(T, N, 256), kt, 0.82, 26.0);
-        for (int c = 1; c <= 16 && (c == 1 || kt / c >= 8); c *= 2) {
+        double best = tiles_us(tiles_of(T, N, 256, 256), kt, 0.82, 26.0);
+        auto take = [&](int form, int chunks, int steps, double us) {
+            if (us >= best) return;
+            best = us;
+            r.form = form;
+            r.chunks = chunks;
+            r.steps = steps;
+        };
+        take(FORM_MID, 1, kt, tiles_us(tiles_of(T, N, 128, 256), kt, 0.5, 9.0));
+        const int64_t small = tiles_of(T, N, 128, 128);
+        if (small <= cus) take(FORM_SMALL, 1, kt, tiles_us(small, kt, 0.27, 8.0));
+        for (int c = 2; c <= 16 && kt / c >= 8; c *= 2) {
             const int steps = (kt + c - 1) / c, chunks = (kt + steps - 1) / steps;
-            const int64_t n = tiles_of(T, N, 128) * chunks;
-            const double t = (chunks == 1 ? small_tiles_us(n, steps, 0.27, 8.0, 0.56) : small_tiles_us(n, steps, 0.37, 4.0, 0.56)) +
-                             partials_us(chunks, (int64_t)T * N);
-            if (t < best) {
-                best = t;
-                r.form = FORM_SMALL;
-                r.chunks = chunks;
-                r.steps = steps;
-            }
+            take(FORM_CHUNKS, chunks, steps, shared_us(small * chunks, steps, 0.37, 0.56) + partials_us(chunks, (int64_t)T * N, 6.0));
         }
     }
     r.forward_bytes = r.chunks > 1 ? (size_t)r.chunks * T * N * 4 : 0;
@@ -218,13 +218,13 @@ static LinearPlan linear_plan(int T, int Kd, int N) {
     // the weight gradient: the rows are the contraction
     const int64_t rt = std::max<int64_t>(1, ((int64_t)T + 31) / 32), out = (int64_t)Kd * N;
     int steps;
-    split_steps(tiles_of(Kd, N, 256), rt, &r.dw_chunks, &steps);
-    double best = big_tiles_us(tiles_of(Kd, N, 256) * r.dw_chunks, steps, 0.8, 11.0) + partials_us(r.dw_chunks, out);
+    split_steps(tiles_of(Kd, N, 256, 256), rt, &r.dw_chunks, &steps);
+    double dw_best = tiles_us(tiles_of(Kd, N, 256, 256) * r.dw_chunks, steps, 0.8, 11.0) + partials_us(r.dw_chunks, out, 2.0);
     for (int c = 1; c <= 32 && (c == 1 || rt / c >= 8); c *= 2) {
         const int st = (int)((rt + c - 1) / c), chunks = (int)((rt + st - 1) / st);
-        const double t = small_tiles_us(tiles_of(Kd, N, 128) * chunks, st, 0.45, 4.0, 0.62) + partials_us(chunks, out);
-        if (t < best) {
-            best = t;
+        const double t = shared_us(tiles_of(Kd, N, 128, 128) * chunks, st, 0.45, 0.62) + partials_us(chunks, out, 2.0);
+        if (t < dw_best) {
+            dw_best = t;
             r.dw_small = true;
             r.dw_chunks = chunks;
             steps = st;
@@ -277,9 +277,9 @@ static int linear_gemm(const LinearParams& l, const LinearPlan& r, hipStream_t s
     p.bias = l.bias;
     p.res = l.res;
     p.act = l.act;
-    if (r.form == FORM_SMALL && tiles_of(l.T, l.N, 128) <= moe_host::num_cus())
-        return launch_cfg<128, 128, 32, 2, 2, LAY_MN, EPI_LINEAR, SCHED_ROWS, kDeepBudget>(p, s);
-    if (r.form == FORM_SMALL) return launch_cfg<128, 128, 32, 2, 2, LAY_MN, EPI_LINEAR, SCHED_ROWS, kLdsBudget>(p, s);
+    // eight waves, two a SIMD, run these tiles 5 to 20% faster than four
+    if (r.form == FORM_SMALL) return launch_cfg<128, 128, 32, 2, 4, LAY_MN, EPI_LINEAR, SCHED_ROWS, kDeepBudget>(p, s);
+    if (r.form == FORM_MID) return launch_cfg<128, 256, 32, 2, 4, LAY_MN, EPI_LINEAR, SCHED_ROWS, kLdsBudget>(p, s);
     return launch_cfg<256, 256, 32, 2, 2, LAY_MN, EPI_LINEAR, SCHED_ROWS, kLdsBudget>(p, s);
 }
 
@@ -368,9 +368,10 @@ extern "C" int moe_linear_backward(const moe_bf16* dy, const moe_bf16* x, int T,
         p.Kd = N;
         p.c = dx;
         p.ldc = Kd;
-        const int64_t n = tiles_of(T, Kd, 128);
-        const bool small = small_tiles_us(n, N / 32, 0.27, 8.0, 0.56) < big_tiles_us(tiles_of(T, Kd, 256), N / 32, 0.82, 12.0);
-        rc = small ? launch_rows_kc_small(p, n <= moe_host::num_cus(), s) : launch_rows_kc(p, EPI_BF16, s);
+        const int64_t n = tiles_of(T, Kd, 128, 128), cus = moe_host::num_cus();
+        const bool small = (n <= cus ? tiles_us(n, N / 32, 0.27, 8.0) : shared_us(n, N / 32, 0.0, 0.56)) <
+                           tiles_us(tiles_of(T, Kd, 256, 256), N / 32, 0.82, 12.0);
+        rc = small ? launch_rows_kc_small(p, n <= cus, s) : launch_rows_kc(p, EPI_BF16, s);
         if (rc != MOE_OK) return rc;
     }
     if (!dw) return MOE_OK;
