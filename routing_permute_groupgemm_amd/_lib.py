@@ -839,6 +839,13 @@ def _ws(ws, need, dev, stream):
     return _empty(need, torch.uint8, dev, stream, result=False), need
 
 
+def _like(t, shape, dtype, name, dev, stream, like):
+    """_out for a buffer of a type that the tensor `like` has too, whose allocator is the shorter way to a new one."""
+    if t is None and stream is None and like.dtype is dtype:
+        return torch.empty_like(like) if like.shape == shape else like.new_empty(shape)
+    return _out(t, shape, dtype, name, dev, stream)
+
+
 def _rank2(t, name):
     if t.dim() != 2:
         raise MoeError(f"{name}: expected 2 dimensions, got {tuple(t.shape)}")
@@ -875,8 +882,8 @@ def moe_layer_few(logits, x, K, e_begin, w_gate, w_up, w_down, residual=None, to
     res = _given(residual, (T, H), torch.bfloat16, "residual", dev)
     K = int(K)
     topk_idx = _out(topk_idx, (T, max(K, 0)), torch.int32, "topk_idx", dev, stream)
-    gates = _out(gates, (T, max(K, 0)), torch.float32, "gates", dev, stream)
-    out = _out(out, (T, H), torch.bfloat16, "out", dev, stream)
+    gates = _like(gates, (T, max(K, 0)), torch.float32, "gates", dev, stream, logits)
+    out = _like(out, (T, H), torch.bfloat16, "out", dev, stream, x)
     lib = load()
     ws, size = _ws(ws, lib.moe_layer_few_workspace_size(T, K, EL, H, F), dev, stream)
     _check(lib.moe_layer_few(_ptr(logits), _ptr(x), T, E, K, int(e_begin), EL, _ptr(w_gate), _ptr(w_up), _ptr(w_down), H, F,
@@ -904,8 +911,8 @@ def moe_layer_norm(x, weight=None, bias=None, add=None, eps=1e-5, rms=False, sum
     if rms and mean is not None:
         raise MoeError("mean: there is none with rms")
     if add is not None or sum is not None:
-        sum = _out(sum, (T, H), x.dtype, "sum", dev, stream)
-    y = _out(y, (T, H), torch.bfloat16, "y", dev, stream)
+        sum = _like(sum, (T, H), x.dtype, "sum", dev, stream, x)
+    y = _like(y, (T, H), torch.bfloat16, "y", dev, stream, x)
     if not rms:
         mean = _out(mean, (T,), torch.float32, "mean", dev, stream)
     rstd = _out(rstd, (T,), torch.float32, "rstd", dev, stream)
@@ -936,9 +943,9 @@ def moe_layer_norm_backward(dy, s, weight, mean, rstd, d_sum=None, rms=False, wa
     want_db = (not rms) if want_db is None else want_db
     if rms and (want_db or db is not None):
         raise MoeError("db: there is no bias with rms")
-    dx = _out(dx, (T, H), s.dtype, "dx", dev, stream)
-    dw = _out(dw, (H,), torch.float32, "dw", dev, stream) if want_dw or dw is not None else None
-    db = _out(db, (H,), torch.float32, "db", dev, stream) if want_db or db is not None else None
+    dx = _like(dx, (T, H), s.dtype, "dx", dev, stream, s)
+    dw = _like(dw, (H,), torch.float32, "dw", dev, stream, rstd) if want_dw or dw is not None else None
+    db = _like(db, (H,), torch.float32, "db", dev, stream, rstd) if want_db or db is not None else None
     lib = load()
     need = lib.moe_layer_norm_backward_workspace_size(T, H) if dw is not None or db is not None else 0
     ws, size = _ws(ws, need, dev, stream)
@@ -969,8 +976,8 @@ def moe_linear(x, w, bias=None, act="none", residual=None, want_z=False, z=None,
     b = _given(bias, (N,), torch.float32, "bias", dev)
     res = _given(residual, (T, N), torch.bfloat16, "residual", dev)
     code = _act(act)
-    z = _out(z, (T, N), torch.bfloat16, "z", dev, stream) if want_z or z is not None else None
-    y = _out(y, (T, N), torch.bfloat16, "y", dev, stream)
+    z = _like(z, (T, N), torch.bfloat16, "z", dev, stream, x) if want_z or z is not None else None
+    y = _like(y, (T, N), torch.bfloat16, "y", dev, stream, x)
     lib = load()
     ws, size = _ws(ws, lib.moe_linear_workspace_size(T, Kd, N), dev, stream)
     _check(lib.moe_linear(_ptr(x), T, Kd, _ptr(w), N, b, code, res, _ptr(z), _ptr(y), _ptr(ws), size,
@@ -998,12 +1005,12 @@ def moe_linear_backward(dy, x, w, act="none", z=None, want_dx=True, want_dw=True
         if z is None:
             raise MoeError("z: the backward of an activation needs the forward's")
         zp = _given(z, (T, N), torch.bfloat16, "z", dev)
-        dz = _out(dz, (T, N), torch.bfloat16, "dz", dev, stream)
+        dz = _like(dz, (T, N), torch.bfloat16, "dz", dev, stream, dy)
     else:
         if dz is not None and dz is not dy:
             raise MoeError("dz: it is dy itself without an activation")
         zp, dz = None, None
-    dx = _out(dx, (T, Kd), torch.bfloat16, "dx", dev, stream) if want_dx or dx is not None else None
+    dx = _like(dx, (T, Kd), torch.bfloat16, "dx", dev, stream, x) if want_dx or dx is not None else None
     dw = _out(dw, (Kd, N), torch.float32, "dw", dev, stream) if want_dw or dw is not None else None
     db = _out(db, (N,), torch.float32, "db", dev, stream) if want_db or db is not None else None
     lib = load()
