@@ -9,7 +9,7 @@
 //
 //   few_up    every workgroup routes the T tokens itself (T <= 64, so an expert's
 //             tokens are a 64-bit mask and a token's row among them a popcount), then
-//             takes blocks of 64 columns of gate and up of the experts that have
+//             takes blocks of columns of gate and up of the experts that have
 //             tokens.  Its waves take the contraction's steps in turn; their sums
 //             meet in LDS, in wave order.  Workgroup 0 also writes the choices, the
 //             gates and the plan that the second kernel reads, and clears its counters.
@@ -18,8 +18,10 @@
 //             forms the tokens' gated sums there, so no third launch is needed.
 //             Which one that is does not change what is added in which order.
 // A row's bits do not depend on the other tokens of the call.
-#include "rows_stream.hpp"
+#include <math.h>
+
 #include "route_select.hpp"
+#include "rows_stream.hpp"
 
 using moe_host::misaligned;
 
@@ -27,7 +29,8 @@ namespace moe {
 
 constexpr int kFewT = 64;
 constexpr int kFewGroups = 512;
-constexpr int kFewUpCols = 64, kFewDownCols = 128;
+constexpr int kFewDownCols = 128;
+constexpr int few_up_cols(bool wide) { return wide ? 128 : 64; }
 
 // An expert with tokens: its rows row0 .. row0+rows-1 of the expert-grouped order.
 struct FewExpert {
@@ -164,22 +167,28 @@ __device__ __forceinline__ void route_few(const FewParams& p, FewPlan& s, bool w
 // of 256 experts.  (The down kernel did not gain from it.)
 __device__ __forceinline__ int xcd_order(int b, int run) { return (b & 7) * run + (b >> 3); }
 
-template <int MT, int S, int W, bool NTL>
+// A wave of a narrow block has 64 columns of both matrices and every W-th step of the contraction; of a wide one, 128
+// columns of one matrix (the first half of the waves gate, the second up) and every W/2-th step.
+template <int MT, int S, int W, bool WIDE, bool NTL>
 __global__ __launch_bounds__(64 * W) void few_up(FewParams p) {
     __shared__ FewPlan plan;
-    __shared__ __attribute__((aligned(16))) WaveSums<2, 4, W> sums;
+    constexpr int MATS = WIDE ? 1 : 2, CW = WIDE ? 8 : 4, KW = WIDE ? W / 2 : W;
+    constexpr int kCols = few_up_cols(WIDE), kQuads = kCols / 4;
+    __shared__ __attribute__((aligned(16))) WaveSums<MATS, CW, W> sums;
     route_few<W>(p, plan, blockIdx.x == 0);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int slabs = p.F / kFewUpCols;
+    const int slabs = (p.F + kCols - 1) / kCols;
     const int total = plan.n_active * slabs, run = (total + 7) / 8;
     for (int b = blockIdx.x; b < 8 * run; b += gridDim.x) {
         const int id = xcd_order(b, run);
         if (id >= total) continue;
-        const int a = id / slabs, col0 = (id - a * slabs) * kFewUpCols;
+        const int a = id / slabs, col0 = (id - a * slabs) * kCols;
         const int j = __builtin_amdgcn_readfirstlane((int)plan.expert[a]);
         const int64_t at = (int64_t)j * p.H * p.F;
-        const uint16_t* const w[2] = {p.w_gate + at, p.w_up + at};
+        const uint16_t* w[MATS];
+        w[0] = (WIDE && wave >= KW ? p.w_up : p.w_gate) + at;
+        if constexpr (!WIDE) w[1] = p.w_up + at;
         const int end = __builtin_amdgcn_readfirstlane((int)plan.row0[a] + __popcll(plan.mask[j]));
         for (int row0 = __builtin_amdgcn_readfirstlane((int)plan.row0[a]); row0 < end; row0 += 16 * MT) {
             const int rows = min(16 * MT, end - row0);
@@ -187,18 +196,26 @@ __global__ __launch_bounds__(64 * W) void few_up(FewParams p) {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
                 x_at[m] = (uint32_t)plan.token[row0 + min(16 * m + (lane & 15), rows - 1)] * (uint32_t)(p.H * 2);
-            RowStream<2, 4, MT, S, NTL> r;
-            r.run(w, p.F, col0 + 4 * (lane & 15), p.x, x_at, rows, wave, W, p.H / 32);
+            RowStream<MATS, CW, MT, S, NTL> r;
+            // columns past the last are read as the last ones; their sums are not stored
+            r.run(w, p.F, min(col0 + CW * (lane & 15), p.F - CW), p.x, x_at, rows, wave % KW, KW, p.H / 32);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 if (16 * m >= rows) break;
                 __syncthreads();  // the sums of the block before are read
                 sums.put(r, m, wave, lane);
                 __syncthreads();
-                for (int i = tid; i < 256; i += 64 * W) {
-                    const int row = i >> 4, c = (i & 15) * 4;
-                    if (16 * m + row >= rows) continue;
-                    const f32x4 g = sums.get(row, c), u = sums.get(row, 64 + c);
+                for (int i = tid; i < 16 * kQuads; i += 64 * W) {
+                    const int row = i / kQuads, c = (i % kQuads) * 4;
+                    if (16 * m + row >= rows || col0 + c >= p.F) continue;
+                    f32x4 g, u;
+                    if constexpr (WIDE) {
+                        g = sums.template get<0, KW>(row, c);
+                        u = sums.template get<KW, W>(row, c);
+                    } else {
+                        g = sums.get(row, c);
+                        u = sums.get(row, 64 + c);
+                    }
                     float v[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[e] = silu_f(g[e]) * u[e];
@@ -324,40 +341,70 @@ static int few_check(int T, int E, int K, int e_local, int H, int F) {
     return MOE_OK;
 }
 
-template <int MT, int S, int W>
-static int launch_few(const FewParams& p, hipStream_t s) {
-    const int experts = std::min(p.e_local, p.T * p.K);
-    // the weights that the tokens can touch would fill half of the last-level cache (256 MB) or more
-    const bool ntl = (int64_t)experts * 6 * p.H * p.F >= (128ll << 20);
-    const int64_t up = std::max<int64_t>(
-        1, std::min<int64_t>((int64_t)experts * (p.F / kFewUpCols), 16 / W * moe_host::num_cus()));
-    const int64_t down = (int64_t)std::max(experts, 1) * ((p.H + kFewDownCols - 1) / kFewDownCols);
-    if (ntl) few_up<MT, S, W, true><<<(unsigned)up, 64 * W, 0, s>>>(p);
-    else few_up<MT, S, W, false><<<(unsigned)up, 64 * W, 0, s>>>(p);
-    const int rc = moe_host::launch_status();
-    if (rc != MOE_OK) return rc;
-    if (ntl) few_down<MT, S, W, true><<<(unsigned)down, 64 * W, 0, s>>>(p);
-    else few_down<MT, S, W, false><<<(unsigned)down, 64 * W, 0, s>>>(p);
+// The weights that the tokens can touch would fill half of the last-level cache (256 MB) or more.
+static bool few_stream(const FewParams& p) {
+    return (int64_t)std::min(p.e_local, p.T * p.K) * 6 * p.H * p.F >= (128ll << 20);
+}
+
+template <int MT, int S, int W, bool WIDE>
+static int launch_few_up(const FewParams& p, int per_cu, hipStream_t s) {
+    const int cols = few_up_cols(WIDE), experts = std::min(p.e_local, p.T * p.K);
+    const unsigned grid = (unsigned)std::max<int64_t>(
+        1, std::min<int64_t>((int64_t)experts * ((p.F + cols - 1) / cols), per_cu * moe_host::num_cus()));
+    if (few_stream(p)) few_up<MT, S, W, WIDE, true><<<grid, 64 * W, 0, s>>>(p);
+    else few_up<MT, S, W, WIDE, false><<<grid, 64 * W, 0, s>>>(p);
     return moe_host::launch_status();
 }
 
-// Row tiles a pass over an expert's weights (MT), stages (S) and waves a workgroup (W), from the sizes; the numbers are us
-// a call (H = 4096, F = 1536, E = 128, K = 8 if nothing else is said).
-//   MT  one tile of 16 rows: an expert with more takes another pass over its weights, which is rare while T*K/E, the
-//       rows that it has on average, are few (64 tokens on 32 of 256 experts, H = 7168, F = 2048: 487, and 589 with four
-//       tiles, whose sums cost the registers of loads in flight).  From 16 on, as many tiles as T can need (64 tokens on
-//       all of 8 experts: 145 with four, 278 with one).
-//   W   4; 8 where the routing (each wave takes T/W tokens) or the rows' loads count, from T > 32 or 8 rows an expert
-//       (64 tokens of the former: 487 against 524; 16 on all of 8 experts: 75 against 80; but one token 69.2 against 67.8).
-//   S   3 where gate and up have at most one workgroup a CU (one token: 67.8, and 70.6 with 2), or with W = 8 and one
-//       tile (487 against 497); else 2 (8 tokens of the former: 170 against 176, 4 tokens 200 against 205).
-static int launch_few_rows(const FewParams& p, hipStream_t s) {
-    const int rows = p.T * p.K / p.E;
-    if (rows >= 16 && p.T > 32) return launch_few<4, 2, 8>(p, s);
-    if (rows >= 16 && p.T > 16) return launch_few<2, 2, 8>(p, s);
-    if (rows >= 8 || p.T > 32) return launch_few<1, 3, 8>(p, s);
-    if ((int64_t)std::min(p.e_local, p.T * p.K) * (p.F / kFewUpCols) <= moe_host::num_cus()) return launch_few<1, 3, 4>(p, s);
-    return launch_few<1, 2, 4>(p, s);
+template <int MT, int S, int W>
+static int launch_few_down(const FewParams& p, hipStream_t s) {
+    const int experts = std::max(1, std::min(p.e_local, p.T * p.K));
+    const unsigned grid = (unsigned)experts * ((p.H + kFewDownCols - 1) / kFewDownCols);
+    if (few_stream(p)) few_down<MT, S, W, true><<<grid, 64 * W, 0, s>>>(p);
+    else few_down<MT, S, W, false><<<grid, 64 * W, 0, s>>>(p);
+    return moe_host::launch_status();
+}
+
+// Row tiles a pass over an expert's weights (MT), stages (S), waves a workgroup (W) and the width of gate and up's blocks,
+// from the sizes; the numbers are us a call.  A: H = 4096, F = 1536, 128 experts, B: H = 2048, F = 768, 128 experts, C: H =
+// 7168, F = 2048, 32 of 256 experts, top 8 each; D: A with 8 experts, all of them chosen.
+//   MT    one tile of 16 rows: an expert with more takes another pass over its weights, which is rare while T*K/E, the
+//         rows that it has on average, are few (C, 64 tokens: 487, and 589 with four tiles, whose sums cost the registers
+//         of loads in flight).  From 16 on, as many tiles as T can need (D, 64 tokens: 145 with four, 278 with one).
+//   W     down 4 (B, 64 tokens 244 in all, 241 with 8 and 270 with 2; 16 tokens 150, 156, 161); 8 where the rows' loads count,
+//         from 8 rows an expert (D, 16 tokens: 75 against 80 with 4).  up as below.
+//   width A wide block (W = 8) reads pieces of 256 bytes of a matrix row, a narrow one of 128, but there are half as many.
+//         With one a CU and up to a CU's worth they gain (A, 2 tokens: 115 against 135; C, 8: 147 against 162), and where
+//         there are so many that an uneven end does not count (A, 64 tokens: 821 against 875; B, 64: 240 against 260; C,
+//         64: 457 against 481), not with few (A, one token: 90 against 68), nor with a few more than CUs (A, 4 tokens: 211
+//         against 199).  How many experts will have a token is taken from a uniform router.
+//   narrow: W = 4, 8 from T > 32 (each wave routes T/W tokens); S = 3 with at most one workgroup a CU (A, one token: 67.8,
+//         and 70.6 with 2) and for W = 8, else 2 (A, 4 tokens 200 against 205).
+//   wide: two workgroups a CU and S = 2, from T > 32 one, which routes once, and S = 4 (A, 16 tokens 534 against 540; C, 64
+//         tokens 468 against 457).
+static int launch_few(const FewParams& p, hipStream_t s) {
+    const int rows = p.T * p.K / p.E, cus = moe_host::num_cus();
+    int rc;
+    if (rows >= 16 && p.T > 32) {
+        rc = launch_few_up<4, 2, 8, false>(p, 2, s);
+        return rc != MOE_OK ? rc : launch_few_down<4, 2, 8>(p, s);
+    }
+    if (rows >= 16 && p.T > 16) {
+        rc = launch_few_up<2, 2, 8, false>(p, 2, s);
+        return rc != MOE_OK ? rc : launch_few_down<2, 2, 8>(p, s);
+    }
+    if (rows >= 8) {
+        rc = launch_few_up<1, 3, 8, false>(p, 2, s);
+        return rc != MOE_OK ? rc : launch_few_down<1, 3, 8>(p, s);
+    }
+    const double active = p.e_local * (1.0 - pow(1.0 - (double)p.K / p.E, p.T));
+    const double blocks = active * ((p.F + 127) / 128);
+    const bool wide = (blocks >= 0.4 * cus && blocks <= 1.03 * cus) || blocks >= 1.7 * cus;
+    if (wide) rc = p.T > 32 ? launch_few_up<1, 4, 8, true>(p, 1, s) : launch_few_up<1, 2, 8, true>(p, 2, s);
+    else if (p.T > 32) rc = launch_few_up<1, 3, 8, false>(p, 2, s);
+    else if (std::min(p.e_local, p.T * p.K) * (p.F / 64) <= cus) rc = launch_few_up<1, 3, 4, false>(p, 3, s);
+    else rc = launch_few_up<1, 2, 4, false>(p, 4, s);
+    return rc != MOE_OK ? rc : launch_few_down<1, 3, 4>(p, s);
 }
 
 }  // namespace moe
@@ -408,5 +455,5 @@ extern "C" int moe_layer_few(const float* logits, const moe_bf16* x, int T, int 
     p.pos = (int*)(b + z.pos);
     p.h = (uint16_t*)(b + z.h);
     p.y = (float*)(b + z.y);
-    return launch_few_rows(p, (hipStream_t)stream);
+    return launch_few(p, (hipStream_t)stream);
 }

@@ -121,11 +121,12 @@ struct WaveSums {
                     *(f32x4*)&v[wave][row][q * 16 * CW + CW * (4 * g + c) + t] =
                         f32x4{r.acc[q][t][m][c], r.acc[q][t + 1][m][c], r.acc[q][t + 2][m][c], r.acc[q][t + 3][m][c]};
     }
-    // 4 columns of a row, the waves added in order
+    // 4 columns of a row, the waves W0 .. W1-1 added in order
+    template <int W0 = 0, int W1 = W>
     __device__ __forceinline__ f32x4 get(int row, int col) const {
-        f32x4 s = *(const f32x4*)&v[0][row][col];
+        f32x4 s = *(const f32x4*)&v[W0][row][col];
 #pragma unroll
-        for (int w = 1; w < W; ++w) s += *(const f32x4*)&v[w][row][col];
+        for (int w = W0 + 1; w < W1; ++w) s += *(const f32x4*)&v[w][row][col];
         return s;
     }
 };

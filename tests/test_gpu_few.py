@@ -66,6 +66,8 @@ CASES = [
     (48, 64, 64, 8, 0, 2, 8),
     (64, 192, 128, 512, 100, 200, 16),
     (64, 448, 576, 9, 0, 9, 9),
+    (64, 64, 64, 512, 0, 512, 16),
+    (20, 128, 1088, 2, 1, 1, 2),
 ]
 
 
@@ -133,6 +135,30 @@ def test_ties_go_to_the_lowest_expert():
     idx = _lib.moe_layer_few(logits, x, K, 0, wg, wu, wd)[1].cpu()
     for t, row in enumerate(logits.cpu().tolist()):
         assert idx[t].tolist() == sorted(range(E), key=lambda e: (-row[e], e))[:K]
+
+
+def test_scores_of_minus_infinity_and_nan():
+    """A router that masks experts gives them -inf: more choices than experts are left get a gate of 0, and a token with
+    none left, or with a NaN, gates that are NaN, as the layer's routing says; the other tokens are as they were."""
+    T, K = 12, 4
+    logits, x, wg, wu, wd = layer(12, T, 128, 64, 70, 70)
+    inf = float("inf")
+    logits[1, 2:] = -inf  # two experts left of four wanted
+    logits[2] = -inf
+    logits[3, 5] = float("nan")
+    logits[4, 7] = inf
+    out, idx, gates = _lib.moe_layer_few(logits, x, K, 0, wg, wu, wd)
+    r_idx, r_gates = _lib.moe_route(logits, K)
+    rows = [t for t in range(T) if t != 3]  # where a NaN is ranked is not said
+    assert torch.equal(idx[rows], r_idx[rows])
+    assert torch.equal(gates[rows].view(torch.int32), r_gates[rows].view(torch.int32))
+    assert idx[1].tolist()[2:] == [2, 3] and (gates[1, 2:] == 0).all() and torch.isnan(gates[2]).all()
+    assert ((idx >= 0) & (idx < 70)).all()
+    fine = [0, 1] + list(range(5, T))
+    clean = logits.clone()
+    clean[2:5] = 0.0
+    assert torch.equal(out[fine], _lib.moe_layer_few(clean, x, K, 0, wg, wu, wd)[0][fine])
+    assert torch.isfinite(out[fine]).all()
 
 
 def test_a_token_does_not_change_with_the_others():

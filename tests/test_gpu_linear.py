@@ -40,7 +40,8 @@ def slope64(act, z):
 # rows and columns that fill no tile
 SHAPES = [(1, 64, 64), (1, 2048, 7168), (2, 64, 192), (15, 512, 320), (16, 1088, 128), (17, 4096, 64), (32, 256, 1536),
           (33, 320, 192), (41, 4096, 1536), (64, 192, 4160), (64, 64, 576), (65, 64, 64), (65, 2048, 320), (200, 7168, 256),
-          (130, 192, 2112), (700, 1536, 832), (1000, 64, 4096), (4001, 2048, 768), (8200, 128, 2112), (16400, 64, 320)]
+          (130, 192, 2112), (700, 1536, 832), (1000, 64, 4096), (4001, 2048, 768), (8200, 128, 2112), (16400, 64, 320),
+          (4000, 4096, 4032)]
 
 
 @pytest.mark.parametrize("T,Kd,N", SHAPES)

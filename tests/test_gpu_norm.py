@@ -27,7 +27,9 @@ def stats(s, eps, rms):
 
 
 SHAPES = [(1, 64), (3, 64), (2, 128), (5, 448), (7, 512), (300, 576), (33, 1024), (1, 2048), (400, 2048), (19, 2112),
-          (500, 2112), (1, 7168), (300, 7168), (4, 8192), (290, 8192), (2, 8256), (270, 8256), (1, 16384), (259, 16384)]
+          (500, 2112), (1, 7168), (300, 7168), (4, 8192), (290, 8192), (2, 8256), (270, 8256), (1, 16384), (259, 16384),
+          # one row a CU and one more, and passes that go past the caches
+          (256, 1024), (257, 1024), (9001, 2048), (3001, 7168)]
 
 
 @pytest.mark.parametrize("T,H", SHAPES)
