@@ -89,30 +89,43 @@ __global__ __launch_bounds__(256) void linear_finish(LinearParams p, int chunks)
     }
 }
 
-// dz = bf16(dy * act'(z)) (dz NULL: not written) and partial column sums of the unrounded products: a workgroup takes
-// 512 columns (64 threads of 8) of the rows blockIdx.y * 4 + r, + 4 * gridDim.y, ...; its four strands of rows meet in
-// LDS.
-__global__ __launch_bounds__(256) void linear_slope(const uint16_t* dy, const uint16_t* __restrict__ z,
-                                                    int64_t T, int N, int act, uint16_t* dz, float* __restrict__ part) {
+// dz = bf16(dy * act'(z)) (dz NULL: not written) and column sums of the unrounded products (part NULL: not wanted; a row
+// of N for each blockIdx.y): a workgroup takes 512 columns (64 threads of 8) of blocks of 16 rows, a strand of 64 threads
+// four rows of each, which are asked for together; the four strands' sums meet in LDS.  dz may be dy: a thread's rows are
+// read before they are written.  Bound by its bytes (131072 x 7168 without an activation, one array read: 283 us; with
+// ReLU, three arrays moved: 738), with GELU by its exponentials (1103).
+template <bool NT>
+__global__ __launch_bounds__(256) void linear_slope(const uint16_t* dy, const uint16_t* __restrict__ z, int64_t T, int N,
+                                                    int act, uint16_t* dz, float* __restrict__ part) {
+    constexpr int R = 4;
     __shared__ __attribute__((aligned(16))) float merge[3][512];
     const int lane = threadIdx.x & 63, strand = threadIdx.x >> 6;
     const int n = (int)blockIdx.x * 512 + lane * 8;
     float sum[8] = {};
     if (n < N) {
-        for (int64_t t = (int64_t)blockIdx.y * 4 + strand; t < T; t += 4 * (int64_t)gridDim.y) {
-            const u32x4 d = *(const u32x4*)(dy + t * N + n);
-            u32x4 v = {};
-            if (act != MOE_ACT_NONE) v = *(const u32x4*)(z + t * N + n);
-            float f[8];
+        for (int64_t t0 = (int64_t)blockIdx.y * 4 * R + strand * R; t0 < T; t0 += 4 * R * (int64_t)gridDim.y) {
+            u32x4 d[R], v[R] = {};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                f[i] = i & 1 ? bf_hi(d[i >> 1]) : bf_lo(d[i >> 1]);
-                if (act != MOE_ACT_NONE) f[i] *= slope(i & 1 ? bf_hi(v[i >> 1]) : bf_lo(v[i >> 1]), act);
-                sum[i] += f[i];
+            for (int r = 0; r < R; ++r) {
+                const int64_t at = min(t0 + r, T - 1) * N + n;
+                d[r] = NT ? __builtin_nontemporal_load((const u32x4*)(dy + at)) : *(const u32x4*)(dy + at);
+                if (act != MOE_ACT_NONE)
+                    v[r] = NT ? __builtin_nontemporal_load((const u32x4*)(z + at)) : *(const u32x4*)(z + at);
             }
-            if (dz)
-                *(u32x4*)(dz + t * N + n) = u32x4{pack_bf2x(f[0], f[1]), pack_bf2x(f[2], f[3]), pack_bf2x(f[4], f[5]),
-                                                  pack_bf2x(f[6], f[7])};
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (t0 + r >= T) break;
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    f[i] = i & 1 ? bf_hi(d[r][i >> 1]) : bf_lo(d[r][i >> 1]);
+                    if (act != MOE_ACT_NONE) f[i] *= slope(i & 1 ? bf_hi(v[r][i >> 1]) : bf_lo(v[r][i >> 1]), act);
+                    sum[i] += f[i];
+                }
+                if (dz)
+                    *(u32x4*)(dz + (t0 + r) * N + n) = u32x4{pack_bf2x(f[0], f[1]), pack_bf2x(f[2], f[3]),
+                                                             pack_bf2x(f[4], f[5]), pack_bf2x(f[6], f[7])};
+            }
         }
     }
     if (!part) return;
@@ -212,9 +225,11 @@ static LinearPlan linear_plan(int T, int Kd, int N) {
         }
     }
     r.forward_bytes = r.chunks > 1 ? (size_t)r.chunks * T * N * 4 : 0;
+    // up to 32 rows one row block, whose column sums are db itself: no partial rows and no launch that adds them (30 x 192
+    // 5.6 us, 65 x 1536 in two launches 6.1, 64 x 1536 in one 9.8)
     const int64_t blocks = (N + 511) / 512;
-    r.slope_rows = (int)std::max<int64_t>(1, std::min<int64_t>(((int64_t)T + 15) / 16, 4 * cus / blocks));
-    r.db_bytes = round256((size_t)r.slope_rows * N * 4);
+    r.slope_rows = T <= 32 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(((int64_t)T + 15) / 16, 4 * cus / blocks));
+    r.db_bytes = r.slope_rows > 1 ? round256((size_t)r.slope_rows * N * 4) : 0;
     // the weight gradient: the rows are the contraction
     const int64_t rt = std::max<int64_t>(1, ((int64_t)T + 31) / 32), out = (int64_t)Kd * N;
     int steps;
@@ -337,20 +352,24 @@ extern "C" int moe_linear_backward(const moe_bf16* dy, const moe_bf16* x, int T,
         return MOE_EALIGN;
     const LinearPlan r = linear_plan(T, Kd, N);
     const bool split = r.dw_chunks > 1;
-    const size_t need = dw && split ? r.backward_bytes : db ? r.db_bytes : 0;
+    const bool rows = db && T > 0 && r.slope_rows > 1;  // partial rows of db
+    const size_t need = dw && split ? r.backward_bytes : rows ? r.db_bytes : 0;
     if (need && (!ws || ws_bytes < need)) return MOE_EWORKSPACE;
     hipStream_t s = (hipStream_t)stream;
     float* db_part = (float*)ws;
     float* dw_part = (float*)((char*)ws + r.db_bytes);
     int rc;
     if (T > 0 && (db || !none)) {
-        linear_slope<<<dim3((N + 511) / 512, r.slope_rows), 256, 0, s>>>(dy, z, T, N, act, none ? nullptr : dz,
-                                                                        db ? db_part : nullptr);
+        const dim3 grid((N + 511) / 512, r.slope_rows);
+        // arrays that fill half of the last-level cache (256 MB) pass it by
+        const bool nt = (int64_t)T * N * (none ? 2 : 4) >= (128ll << 20);
+        if (nt) linear_slope<true><<<grid, 256, 0, s>>>(dy, z, T, N, act, none ? nullptr : dz, rows ? db_part : db);
+        else linear_slope<false><<<grid, 256, 0, s>>>(dy, z, T, N, act, none ? nullptr : dz, rows ? db_part : db);
         rc = moe_host::launch_status();
         if (rc != MOE_OK) return rc;
     }
-    if (db) {
-        rc = moe_host::column_sums(db_part, T > 0 ? r.slope_rows : 0, N, N, db, nullptr, s);
+    if (rows || (db && T == 0)) {
+        rc = moe_host::column_sums(db_part, rows ? r.slope_rows : 0, N, N, db, nullptr, s);
         if (rc != MOE_OK) return rc;
     }
     const uint16_t* d = none ? dy : dz;
