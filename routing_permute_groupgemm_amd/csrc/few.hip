@@ -370,7 +370,9 @@ static int launch_few_down(const FewParams& p, hipStream_t s) {
 // 7168, F = 2048, 32 of 256 experts, top 8 each; D: A with 8 experts, all of them chosen.
 //   MT    one tile of 16 rows: an expert with more takes another pass over its weights, which is rare while T*K/E, the
 //         rows that it has on average, are few (C, 64 tokens: 487, and 589 with four tiles, whose sums cost the registers
-//         of loads in flight).  From 16 on, as many tiles as T can need (D, 64 tokens: 145 with four, 278 with one).
+//         of loads in flight; A with 16 experts, top 4, 24 tokens: 119, and 132 with two).  From 8 on two (the same, 64
+//         tokens: 154, 198 with four; 48 tokens: 144, 176 with one; D, top 2, 64: 84, 108 with four), from 32 on four
+//         (D, 64 tokens: 144, 278 with one).
 //   W     down 4 (B, 64 tokens 244 in all, 241 with 8 and 270 with 2; 16 tokens 150, 156, 161); 8 where the rows' loads count,
 //         from 8 rows an expert (D, 16 tokens: 75 against 80 with 4).  up as below.
 //   width A wide block (W = 8) reads pieces of 256 bytes of a matrix row, a narrow one of 128, but there are half as many.
@@ -380,16 +382,16 @@ static int launch_few_down(const FewParams& p, hipStream_t s) {
 //         against 199).  How many experts will have a token is taken from a uniform router.
 //   narrow: W = 4, 8 from T > 32 (each wave routes T/W tokens); S = 3 with at most one workgroup a CU (A, one token: 67.8,
 //         and 70.6 with 2) and for W = 8, else 2 (A, 4 tokens 200 against 205).
-//   wide: two workgroups a CU and S = 2, from T > 32 one, which routes once, and S = 4 (A, 16 tokens 534 against 540; C, 64
-//         tokens 468 against 457).
+//   wide: two workgroups a CU and S = 2 (A, 16 tokens: 534, and 540 in the other form), from T > 32 one, which routes
+//         once, and S = 4 (C, 64 tokens: 457, and 468).
 static int launch_few(const FewParams& p, hipStream_t s) {
     const int rows = p.T * p.K / p.E, cus = moe_host::num_cus();
     int rc;
-    if (rows >= 16 && p.T > 32) {
+    if (rows >= 32 && p.T > 32) {
         rc = launch_few_up<4, 2, 8, false>(p, 2, s);
         return rc != MOE_OK ? rc : launch_few_down<4, 2, 8>(p, s);
     }
-    if (rows >= 16 && p.T > 16) {
+    if (rows >= 8 && p.T > 16) {
         rc = launch_few_up<2, 2, 8, false>(p, 2, s);
         return rc != MOE_OK ? rc : launch_few_down<2, 2, 8>(p, s);
     }
