@@ -10,7 +10,7 @@
 // performance model notes that SwiGLU is purely memory-bound, so it is fused
 // into the GEMM epilogue.
 //
-// EPI_LINEAR (dense rows) adds bias, activation and residual to the rows of a product that does not go by expert.
+// EPI_LINEAR and above (dense rows) adds bias, activation and residual to the rows of a product that does not go by expert.
 //
 // The SwiGLU epilogues also come in 8-bit forms, which save (a, b) for the
 // backward, and read it there, in block-scaled bytes (mx.hpp).
@@ -87,8 +87,9 @@ enum : int {
     EPI_F32 = 3,
     EPI_SWIGLU8 = 4,
     EPI_SWIGLU_BWD8 = 5,
-    EPI_LINEAR = 6  // dense rows: bias, activation and residual (linear.hpp)
+    EPI_LINEAR = 16  // dense rows: bias, activation, residual (linear.hpp): + the activation, + 4 with a residual, + 8 with z
 };
+constexpr bool is_linear(int epi) { return epi >= EPI_LINEAR; }
 constexpr bool is_up(int epi) { return epi == EPI_SWIGLU || epi == EPI_SWIGLU8; }
 enum : int { SCHED_ROWS = 0, SCHED_WGRAD = 1 };
 
@@ -133,8 +134,7 @@ struct GemmParams {
     int stagger_phases;
     int8_t* q8;           // SWIGLU8 (out), SWIGLU_BWD8 (in): saved [a | b] in 8 bits, [rows, 2N]
     uint8_t* s8;          // their scale bytes, [rows, 2N/32]
-    const uint16_t* res;  // LINEAR: residual [rows, N], or NULL (c2: the saved z, or NULL)
-    int act;              // LINEAR: moe_act
+    const uint16_t* res;  // LINEAR: residual [rows, N] (c2: the saved z)
 };
 
 typedef __attribute__((ext_vector_type(4))) int i32x4;
@@ -314,7 +314,7 @@ struct Tile {
 // The GEMM of one workgroup for one tile shape.  smem is the stage ring;
 // s_off holds the clamped row offsets (already loaded); s_start and s_wave are
 // scratch for the schedule; s_idx (GATHER only) holds the prefetched source
-// indices of the A rows.  FULLC: every tile's columns (and, for the weight
+// indices of the A rows (EPI_LINEAR: the waves' bias).  FULLC: every tile's columns (and, for the weight
 // gradient, rows) lie inside the output, so the loads skip those bounds
 // checks.  NTB: every expert fits one row tile, so each weight
 // byte is read once and the weight loads carry the non-temporal hint.
@@ -1371,83 +1371,108 @@ __device__ __forceinline__ void gg_body(const GemmParams& p, uint8_t* smem, cons
         }
 
         // ---- epilogue: lane holds row (l%32) and columns 8*j4 + 4*(l/32) + 0..3 ----
-        if constexpr (EPI == EPI_LINEAR) {
-            // Lane l holds row l%32 and columns 8*j4 + 4*(l/32) + 0..3 of a 32 x 32 block.  A swap between the wave's
-            // halves turns two such groups of packed results into 8 neighbouring columns of a row, 16 bytes a lane and 32
-            // bytes of a row an instruction (which the cache merges into lines), and the residual's 16 bytes into the
-            // groups that the sums have: no staging through LDS.  The residual of the whole tile is asked for before the
-            // first store, so that no load waits for a store.  16384 rows x 2048 x 7168 with a residual 535 us (496
-            // without), against 567 through LDS in fp32 and 639 there with the residual loaded block by block: what is
-            // left of the epilogue is mostly its bytes, which all workgroups move at the same time.
+        if constexpr (is_linear(EPI)) {
+            // Results go out through LDS as the plain ones below do, in blocks of 32 rows x 128 bytes (64 where a wave's
+            // share of the free slot is smaller), and the residual comes in the same way: its lines are asked for, the
+            // whole tile's, before the first store (a load issued behind stores also waits for them), and pass through the
+            // block's place in LDS into the sums' layout.  Sums, bias, activation and residual meet in fp32.  The wave's
+            // bias columns wait in LDS (with the residual the registers do not hold them).  16384 rows x 2048 x 7168 take
+            // 404 us, with a residual 455, with GELU 459, with ReLU, residual and z 517; the plain epilogue takes 385 there.
+            constexpr int kSlot = TL::kStage / TL::kWaves;
+            constexpr int kQ = NTW % 2 == 0 && kSlot >= 4096 ? 2 : 1;  // 32-column tiles a block
+            constexpr int kRowBytes = 64 * kQ, kBlock = 32 * kRowBytes, kChunks = 4 * kQ, kRows = 64 / kChunks;
+            constexpr int kRounds = NTW / kQ, kLines = 32 / kRows;
+            constexpr int kBufs = kSlot >= 2 * kBlock && kRounds % 2 == 0 ? 2 : 1;
+            static_assert(kSlot >= kBlock, "staging space per wave");
+            uint8_t* stg = smem + ((gs + S - 1) % S) * TL::kStage + wave * (kBufs * kBlock);
+            // Activation, residual and z are known to the compiler.  With a choice between them here it copies all 256 sums
+            // out of the accumulators in front of the choice, and spills them.  With one at each of their uses the code that
+            // a tile runs through is scattered over more than the instruction cache holds, which cost 100 us of 509 at the
+            // sizes above.  And a path from the residual's loads into the next tile that passes by their use has that tile
+            // wait for all its own loads.
+            constexpr int ACT = (EPI - EPI_LINEAR) & 3;
+            constexpr bool RES = ((EPI - EPI_LINEAR) & 4) != 0, Z = ((EPI - EPI_LINEAR) & 8) != 0;
             const int ln = lane_id_here();
-            const int h = ln >> 5;
-            auto swap_halves = [](uint32_t& a, uint32_t& b) {  // a's upper half of lanes with b's lower half
-                const auto s = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-                a = s[0];
-                b = s[1];
+            const int r = ln & 31, h = ln >> 5, lr = ln / kChunks, lc = ln % kChunks;
+            // 16-byte chunks XOR-swizzled by row
+            auto stage_addr = [&](int buf, int row, int chunk) {
+                return (MOE_LDS uint8_t*)(stg + buf * kBlock + row * kRowBytes +
+                                          ((chunk ^ (kQ == 2 ? row & 7 : (row >> 1) & 3)) << 4));
             };
-            auto packed = [&](const f32x4& lo, const f32x4& hi) {
-                u32x4 v = {pack_bf2x(lo[0], lo[1]), pack_bf2x(lo[2], lo[3]), pack_bf2x(hi[0], hi[1]), pack_bf2x(hi[2], hi[3])};
-                uint32_t a0 = v[0], a1 = v[1], b0 = v[2], b1 = v[3];
-                swap_halves(a0, b0);
-                swap_halves(a1, b1);
-                return u32x4{a0, a1, b0, b1};
+            // of the tile's first row; 256 rows are below 2 GiB
+            const int64_t tile_at = (int64_t)row0 * p.ldc + ni * BN + wn * (BN / WN);
+            const int left = p.N - (ni * BN + wn * (BN / WN));
+            auto line_at = [&](int mt, int np, int i) {
+                return (uint32_t)(row_base(mt) + kRows * i + lr) * (uint32_t)p.ldc + (uint32_t)(32 * kQ * np + 8 * lc);
             };
-            u32x4 res[MTW][NTW][2] = {};
-            if (p.res) {
+            auto inside = [&](int mt, int np, int i) {
+                return row_base(mt) + kRows * i + lr < valid && 32 * kQ * np + 8 * lc < left;
+            };
+            float* bias = (float*)s_idx + wave * (NTW * 32);
+            if (ln < NTW * 8)
+                *(MOE_LDS f32x4*)(bias + 4 * ln) =
+                    p.bias && 4 * ln < left ? *(const f32x4*)(p.bias + p.N - left + 4 * ln) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            auto sum_of = [&](int mt, int np, int q, int j4) {
+                const f32x16& a = acc[mt][np * kQ + q];
+                return f32x4{a[4 * j4], a[4 * j4 + 1], a[4 * j4 + 2], a[4 * j4 + 3]} +
+                       *(const MOE_LDS f32x4*)(bias + 32 * (np * kQ + q) + 8 * j4 + 4 * h);
+            };
+            auto place = [&](int b, int q, int j4) { return (MOE_LDS u32x2*)(stage_addr(b, r, 4 * q + j4) + 8 * h); };
+            auto packed = [&](const f32x4& f) { return u32x2{pack_bf2x(f[0], f[1]), pack_bf2x(f[2], f[3])}; };
+            auto flush = [&](uint16_t* to, int mt, int np0) {
+#pragma unroll
+                for (int b = 0; b < kBufs; ++b)
+#pragma unroll
+                    for (int i = 0; i < kLines; ++i) {
+                        const u32x4 v = *(const MOE_LDS u32x4*)stage_addr(b, kRows * i + lr, lc);
+                        if (inside(mt, np0 + b, i)) *(u32x4*)(to + tile_at + line_at(mt, np0 + b, i)) = v;
+                    }
+            };
+            u32x4 res[MTW][kRounds][kLines] = {};
+            if constexpr (RES) {
+                const uint16_t* from = p.res + tile_at;
 #pragma unroll
                 for (int mt = 0; mt < MTW; ++mt)
 #pragma unroll
-                    for (int nt = 0; nt < NTW; ++nt)
+                    for (int np = 0; np < kRounds; ++np)
 #pragma unroll
-                        for (int jp = 0; jp < 2; ++jp) {
-                            const int mloc = row_base(mt) + (ln & 31), n = ni * BN + col_of(nt) + 16 * jp + 8 * h;
-                            if (mloc < valid && n < p.N)
-                                res[mt][nt][jp] = *(const u32x4*)(p.res + (int64_t)(row0 + mloc) * p.ldc + n);
-                        }
-            }
-            // the wave's bias columns wait in the stage slot that is free until the next stage issues its loads (in
-            // registers they would make the 256-row body spill)
-            static_assert(TL::kStage / TL::kWaves >= NTW * 128, "room for the bias");
-            uint8_t* stg = smem + ((gs + S - 1) % S) * TL::kStage + wave * (NTW * 128);
-            if (ln < NTW * 8) {
-                const int n = ni * BN + col_of(0) + 4 * ln;
-                *(MOE_LDS f32x4*)(stg + 16 * ln) = p.bias && n < p.N ? *(const f32x4*)(p.bias + n) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                        for (int i = 0; i < kLines; ++i)
+                            if (inside(mt, np, i)) res[mt][np][i] = *(const u32x4*)(from + line_at(mt, np, i));
             }
 #pragma unroll
             for (int mt = 0; mt < MTW; ++mt) {
                 __builtin_amdgcn_sched_barrier(0);
-                const int mloc = row_base(mt) + (ln & 31);
 #pragma unroll
-                for (int nt = 0; nt < NTW; ++nt)
+                for (int np0 = 0; np0 < kRounds; np0 += kBufs) {
+                    if constexpr (Z) {
 #pragma unroll
-                    for (int jp = 0; jp < 2; ++jp) {
-                        const f32x16& a = acc[mt][nt];
-                        f32x4 f[2];
+                        for (int b = 0; b < kBufs; ++b)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            f[e] = f32x4{a[8 * jp + 4 * e], a[8 * jp + 4 * e + 1], a[8 * jp + 4 * e + 2], a[8 * jp + 4 * e + 3]} +
-                                   *(const MOE_LDS f32x4*)(stg + 128 * nt + 32 * (2 * jp + e) + 16 * h);
-                        const int n = ni * BN + col_of(nt) + 16 * jp + 8 * h;
-                        const bool in = mloc < valid && n < p.N;
-                        const int64_t at = (int64_t)(row0 + mloc) * p.ldc + n;
-                        if (p.c2) {
-                            const u32x4 z = packed(f[0], f[1]);
-                            if (in) *(u32x4*)(p.c2 + at) = z;
-                        }
-                        activate(f[0], p.act);
-                        activate(f[1], p.act);
-                        if (p.res) {
-                            uint32_t r0 = res[mt][nt][jp][0], r1 = res[mt][nt][jp][1], r2 = res[mt][nt][jp][2],
-                                     r3 = res[mt][nt][jp][3];
-                            swap_halves(r0, r2);
-                            swap_halves(r1, r3);
-                            f[0] += widen4(u32x2{r0, r1});
-                            f[1] += widen4(u32x2{r2, r3});
-                        }
-                        const u32x4 y = packed(f[0], f[1]);
-                        if (in) *(u32x4*)(p.c + at) = y;
+                            for (int q = 0; q < kQ; ++q)
+#pragma unroll
+                                for (int j4 = 0; j4 < 4; ++j4) *place(b, q, j4) = packed(sum_of(mt, np0 + b, q, j4));
+                        flush(p.c2, mt, np0);
                     }
+                    if constexpr (RES) {
+#pragma unroll
+                        for (int b = 0; b < kBufs; ++b)
+#pragma unroll
+                            for (int i = 0; i < kLines; ++i)
+                                *(MOE_LDS u32x4*)stage_addr(b, kRows * i + lr, lc) = res[mt][np0 + b][i];
+                    }
+#pragma unroll
+                    for (int b = 0; b < kBufs; ++b)
+#pragma unroll
+                        for (int q = 0; q < kQ; ++q)
+#pragma unroll
+                            for (int j4 = 0; j4 < 4; ++j4) {
+                                f32x4 f = sum_of(mt, np0 + b, q, j4);
+                                activate<ACT>(f);
+                                if constexpr (RES) f += widen4(*place(b, q, j4));
+                                *place(b, q, j4) = packed(f);
+                            }
+                    flush(p.c, mt, np0);
+                }
             }
             __syncthreads();  // every wave is done with the slot before the next stage refills it
             continue;
@@ -1912,7 +1937,9 @@ void gg_kernel(GemmParams p) {
     __shared__ int s_wave[16];
     // GATHER: two buffers of 64 source indices per A load of each wave, and
     // 1 KiB of slack behind them
-    __shared__ int s_idx[GATHER ? 2 * TL::kALoads * 64 + 256 : 1];
+    // EPI_LINEAR: each wave's bias columns
+    __shared__ alignas(is_linear(EPI) ? 16 : 4) int
+        s_idx[GATHER ? 2 * TL::kALoads * 64 + 256 : is_linear(EPI) ? TL::kWaves * TL::kNTW * 32 : 1];
     __shared__ int s_maxrows;
     // Start stagger, a measurement knob (off unless MOE_GEMM_STAGGER_P > 1 and
     // MOE_GEMM_STAGGER_NS are set): workgroup b waits ((b / 8) % P) * NS
@@ -1937,7 +1964,7 @@ void gg_kernel(GemmParams p) {
     }
     __syncthreads();
     // the non-temporal weight path exists for the forward GEMMs (weights N-contiguous)
-    constexpr bool kNtPath = SCHED == SCHED_ROWS && LB == LAY_MN && EPI != EPI_F32 && EPI != EPI_LINEAR;
+    constexpr bool kNtPath = SCHED == SCHED_ROWS && LB == LAY_MN && EPI != EPI_F32 && !is_linear(EPI);
     if constexpr (kNtPath) {
         for (int j = threadIdx.x; j < p.e_local; j += TL::kThreads) atomicMax(&s_maxrows, s_off[j + 1] - s_off[j]);
         __syncthreads();

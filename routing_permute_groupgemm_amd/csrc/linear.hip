@@ -14,7 +14,7 @@
 // The backward's products are the GroupGEMM's as well; linear_slope forms dz and the partial column sums of db in
 // one pass.
 #include "columns.hpp"
-#include "gemm_kernel.hpp"
+#include "linear_tiles.hpp"
 #include "rows_stream.hpp"
 
 using moe_host::misaligned;
@@ -167,7 +167,7 @@ static int64_t tiles_of(int64_t rows, int64_t cols, int bm, int bn) {
     return ((rows + bm - 1) / bm) * ((cols + bn - 1) / bn);
 }
 
-enum : int { FORM_ROWS = 0, FORM_SMALL = 1, FORM_MID = 2, FORM_BIG = 3, FORM_CHUNKS = 4 };
+enum : int { FORM_ROWS = 0, FORM_SMALL = TILES_SMALL, FORM_MID = TILES_MID, FORM_BIG = TILES_BIG, FORM_CHUNKS = 4 };
 constexpr int kFewRows = 256;
 
 struct LinearPlan {
@@ -208,7 +208,7 @@ static LinearPlan linear_plan(int T, int Kd, int N) {
         r.form = FORM_BIG;
         r.chunks = 1;
         r.steps = kt;
-        double best = tiles_us(tiles_of(T, N, 256, 256), kt, 0.82, 26.0);
+        double best = tiles_us(tiles_of(T, N, 256, 256), kt, 0.8, 10.0);
         auto take = [&](int form, int chunks, int steps, double us) {
             if (us >= best) return;
             best = us;
@@ -291,11 +291,12 @@ static int linear_gemm(const LinearParams& l, const LinearPlan& r, hipStream_t s
     p.c2 = l.z;
     p.bias = l.bias;
     p.res = l.res;
-    p.act = l.act;
-    // eight waves, two a SIMD, run these tiles 5 to 20% faster than four
-    if (r.form == FORM_SMALL) return launch_cfg<128, 128, 32, 2, 4, LAY_MN, EPI_LINEAR, SCHED_ROWS, kDeepBudget>(p, s);
-    if (r.form == FORM_MID) return launch_cfg<128, 256, 32, 2, 4, LAY_MN, EPI_LINEAR, SCHED_ROWS, kLdsBudget>(p, s);
-    return launch_cfg<256, 256, 32, 2, 2, LAY_MN, EPI_LINEAR, SCHED_ROWS, kLdsBudget>(p, s);
+    switch (l.act) {
+        case MOE_ACT_RELU: return launch_linear_relu(p, r.form, s);
+        case MOE_ACT_SILU: return launch_linear_silu(p, r.form, s);
+        case MOE_ACT_GELU: return launch_linear_gelu(p, r.form, s);
+        default: return launch_linear_none(p, r.form, s);
+    }
 }
 
 }  // namespace moe
