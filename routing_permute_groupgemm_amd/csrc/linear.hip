@@ -93,7 +93,7 @@ __global__ __launch_bounds__(256) void linear_finish(LinearParams p, int chunks)
 // of N for each blockIdx.y): a workgroup takes 512 columns (64 threads of 8) of blocks of 16 rows, a strand of 64 threads
 // four rows of each, which are asked for together; the four strands' sums meet in LDS.  dz may be dy: a thread's rows are
 // read before they are written.  Bound by its bytes (131072 x 7168 without an activation, one array read: 283 us; with
-// ReLU, three arrays moved: 738), with GELU by its exponentials (1103).
+// ReLU, three arrays moved: 738), with GELU its arithmetic takes part (815).
 template <bool NT>
 __global__ __launch_bounds__(256) void linear_slope(const uint16_t* dy, const uint16_t* __restrict__ z, int64_t T, int N,
                                                     int act, uint16_t* dz, float* __restrict__ part) {
