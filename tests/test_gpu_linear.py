@@ -71,6 +71,38 @@ def test_forward(T, Kd, N, act):
     assert again is acc and torch.equal(acc, y)
 
 
+# streamed rows, chunks, the three tiles, the largest with whole tiles alone and not
+OPTIONS = [(40, 128, 192), (300, 4096, 320), (1000, 64, 4096), (2000, 2048, 4032), (4000, 128, 4160), (4096, 128, 4096)]
+
+
+@pytest.mark.parametrize("T,Kd,N", OPTIONS)
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_every_set_of_options(T, Kd, N, act, with_bias):
+    """Whether z is wanted changes no bit of y, whether there is a residual none of z; without an activation and a
+    residual y is z; and y without a residual against float64, as above."""
+    x, w = rand(T, T, Kd, dtype=BF), rand(N + 1, Kd, N, std=0.05, dtype=BF)
+    bias, res = rand(3, N) if with_bias else None, rand(4, T, N, dtype=BF)
+    print(f"[linear] options T={T} Kd={Kd} N={N} {act} bias {with_bias}", flush=True)
+    y_res, z = _lib.moe_linear(x, w, bias=bias, act=act, residual=res, want_z=True)
+    assert torch.equal(_lib.moe_linear(x, w, bias=bias, act=act, residual=res)[0], y_res)
+    y, z_too = _lib.moe_linear(x, w, bias=bias, act=act, want_z=True)
+    assert torch.equal(z_too, z)
+    assert torch.equal(_lib.moe_linear(x, w, bias=bias, act=act)[0], y)
+    want = x.double() @ w.double()
+    ez = (Kd + 8) * U * (x.double().abs() @ w.double().abs())
+    if with_bias:
+        want += bias.double()
+        ez += (Kd + 8) * U * bias.double().abs()
+    if act == "none":
+        assert torch.equal(y, z)
+    tol = 1.13 * ez + (2.0 ** -18 if act in ("silu", "gelu") else 0) * want.abs()
+    a = act64(act, want)
+    assert ((y.double() - a).abs() <= tol + 2.0 ** -8 * (a.abs() + tol) + 1e-37).all()
+    tol, a = tol + 2 * U * res.double().abs(), a + res.double()
+    assert ((y_res.double() - a).abs() <= tol + 2.0 ** -8 * (a.abs() + tol) + 1e-37).all()
+
+
 @pytest.mark.parametrize("T,Kd,N", SHAPES)
 def test_exact_on_integers(T, Kd, N):
     """Whole numbers whose sums are exact in fp32 in any order: every output bit for bit, so no row, column or
