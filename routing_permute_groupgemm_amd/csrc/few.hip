@@ -3,7 +3,11 @@
 // combine.
 //
 //   out[t] = bf16(residual[t] + sum over k ascending of gate[t,k] * y[t,k])
-//   y[t,k] = bf16(silu(x_t . Wg_j) * (x_t . Wu_j)) . Wd_j,   j = the k-th expert of token t, if it is local
+//   y[t,k] = h . Wd_j,   h = silu(x_t . Wg_j) * (x_t . Wu_j),   j = the k-th expert of token t, if it is local
+// h is kept as two bf16 values, itself rounded and what that left (16 bits in all), so that the output's rounding is the
+// only one that counts.  The down product reads so few rows that the second costs nothing beside the weights (H = 4096, F =
+// 1536, 128 experts, 64 tokens 827 us without and 836 with it, 16 tokens 532 and 534), but for experts with dozens of rows
+// (8 experts, 64 rows each: 144 and 155).
 // Almost every byte is a weight of an expert that has a token, read once (6*H*F
 // bytes each): the time is that of streaming them.
 //
@@ -17,7 +21,7 @@
 //             the workspace; the last of a column block's workgroups to finish
 //             forms the tokens' gated sums there, so no third launch is needed.
 //             Which one that is does not change what is added in which order.
-// A row's bits do not depend on the other tokens of the call.
+// A token's bits do not depend on the other tokens of the call, nor on how many there are.
 #include <math.h>
 
 #include "route_select.hpp"
@@ -52,7 +56,8 @@ struct FewParams {
     int* arrived;       // [column blocks of the down product]
     FewExpert* active;  // [min(e_local, T*K)]
     int* pos;           // [T*K]: the pair's row, or -1
-    uint16_t* h;        // [rows][F]
+    uint16_t* h;        // [2][rows][F]: rounded to bf16, and the rests
+    uint32_t h_rest;    // bytes from the one to the other
     float* y;           // [rows][H]
 };
 
@@ -219,8 +224,13 @@ __global__ __launch_bounds__(64 * W) void few_up(FewParams p) {
                     float v[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[e] = silu_f(g[e]) * u[e];
-                    *(u32x2*)(p.h + (int64_t)(row0 + 16 * m + row) * p.F + col0 + c) =
-                        u32x2{pack_bf2x(v[0], v[1]), pack_bf2x(v[2], v[3])};
+                    const u32x2 hi = {pack_bf2x(v[0], v[1]), pack_bf2x(v[2], v[3])};
+                    const float top[4] = {bf_lo(hi[0]), bf_hi(hi[0]), bf_lo(hi[1]), bf_hi(hi[1])};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = fabsf(top[e]) < __builtin_inff() ? v[e] - top[e] : 0.0f;
+                    uint16_t* to = p.h + (int64_t)(row0 + 16 * m + row) * p.F + col0 + c;
+                    *(u32x2*)to = hi;
+                    *(u32x2*)((char*)to + p.h_rest) = u32x2{pack_bf2x(v[0], v[1]), pack_bf2x(v[2], v[3])};
                 }
             }
         }
@@ -289,9 +299,9 @@ __global__ __launch_bounds__(64 * W) void few_down(FewParams p) {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
             x_at[m] = (uint32_t)(row0 + min(16 * m + (lane & 15), rows - 1)) * (uint32_t)(p.F * 2);
-        RowStream<1, 8, MT, S, NTL> r;
+        RowStream<1, 8, MT, S, NTL, true> r;
         // columns past the last are read as the last ones; their sums are not stored
-        r.run(w, p.H, min(col0 + 8 * (lane & 15), p.H - 8), p.h, x_at, rows, wave, W, p.F / 32);
+        r.run(w, p.H, min(col0 + 8 * (lane & 15), p.H - 8), p.h, x_at, rows, wave, W, p.F / 32, p.h_rest);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             if (16 * m >= rows) break;
@@ -327,7 +337,7 @@ static FewSizes few_sizes(int T, int K, int e_local, int H, int F) {
     s.active = s.arrived + up256((size_t)(H + kFewDownCols - 1) / kFewDownCols * 4);
     s.pos = s.active + up256(std::min<size_t>(e_local, rows) * sizeof(FewExpert));
     s.h = s.pos + up256((size_t)T * K * 4);
-    s.y = s.h + up256(rows * F * 2);
+    s.y = s.h + up256(rows * F * 4);
     s.total = s.y + up256(rows * H * 4);
     return s;
 }
@@ -365,46 +375,43 @@ static int launch_few_down(const FewParams& p, hipStream_t s) {
     return moe_host::launch_status();
 }
 
-// Row tiles a pass over an expert's weights (MT), stages (S), waves a workgroup (W) and the width of gate and up's blocks,
-// from the sizes; the numbers are us a call.  A: H = 4096, F = 1536, 128 experts, B: H = 2048, F = 768, 128 experts, C: H =
-// 7168, F = 2048, 32 of 256 experts, top 8 each; D: A with 8 experts, all of them chosen.
+// Row tiles a pass over an expert's weights (MT), stages (S) and the width of gate and up's blocks, from the sizes; the
+// numbers are us a call.  A: H = 4096, F = 1536, 128 experts, B: H = 2048, F = 768, 128 experts, C: H = 7168, F = 2048, 32 of
+// 256 experts, top 8 each; D: A with 8 experts, all of them chosen.
+//   waves Four share a contraction in every form (a wide block's eight are four a matrix), so that a token's sums, added in
+//         wave order, do not depend on how many others there are.  Eight would be 6 to 12% faster where the rows' loads count
+//         (D, 16 tokens: 78 against 83; D, top 2, 64 tokens: 86 against 96), and slower elsewhere (B, 64: 268 against 244).
 //   MT    one tile of 16 rows: an expert with more takes another pass over its weights, which is rare while T*K/E, the
-//         rows that it has on average, are few (C, 64 tokens: 487, and 589 with four tiles, whose sums cost the registers
+//         rows that it has on average, are few (C, 64 tokens: 457, and 589 with four tiles, whose sums cost the registers
 //         of loads in flight; A with 16 experts, top 4, 24 tokens: 119, and 132 with two).  From 8 on two (the same, 64
-//         tokens: 154, 198 with four; 48 tokens: 144, 176 with one; D, top 2, 64: 84, 108 with four), from 32 on four
-//         (D, 64 tokens: 144, 278 with one).
-//   W     down 4 (B, 64 tokens 244 in all, 241 with 8 and 270 with 2; 16 tokens 150, 156, 161); 8 where the rows' loads count,
-//         from 8 rows an expert (D, 16 tokens: 75 against 80 with 4).  up as below.
-//   width A wide block (W = 8) reads pieces of 256 bytes of a matrix row, a narrow one of 128, but there are half as many.
-//         With one a CU and up to a CU's worth they gain (A, 2 tokens: 115 against 135; C, 8: 147 against 162), and where
-//         there are so many that an uneven end does not count (A, 64 tokens: 821 against 875; B, 64: 240 against 260; C,
-//         64: 457 against 481), not with few (A, one token: 90 against 68), nor with a few more than CUs (A, 4 tokens: 211
-//         against 199).  How many experts will have a token is taken from a uniform router.
-//   narrow: W = 4, 8 from T > 32 (each wave routes T/W tokens); S = 3 with at most one workgroup a CU (A, one token: 67.8,
-//         and 70.6 with 2) and for W = 8, else 2 (A, 4 tokens 200 against 205).
+//         tokens: 171, over 198 with four; 48 tokens: 159, 176 with one), from 32 on four (D, 64 tokens: 154, 278 with
+//         one).
+//   width A wide block reads pieces of 256 bytes of a matrix row, a narrow one of 128, but there are half as many.  With one
+//         a CU and up to a CU's worth they gain (A, 2 tokens: 115 against 135; C, 8: 147 against 162), and where there are
+//         so many that an uneven end does not count (A, 64 tokens: 821 against 875; B, 64: 240 against 260; C, 64: 457
+//         against 481), not with few (A, one token: 90 against 68), nor with a few more than CUs (A, 4 tokens: 211 against
+//         199).  How many experts will have a token is taken from a uniform router.
+//   narrow: S = 3 with at most one workgroup a CU (A, one token: 67.8, and 70.6 with 2) and for T > 32, else 2 (A, 4 tokens
+//         200 against 205).
 //   wide: two workgroups a CU and S = 2 (A, 16 tokens: 534, and 540 in the other form), from T > 32 one, which routes
 //         once, and S = 4 (C, 64 tokens: 457, and 468).
 static int launch_few(const FewParams& p, hipStream_t s) {
     const int rows = p.T * p.K / p.E, cus = moe_host::num_cus();
     int rc;
     if (rows >= 32 && p.T > 32) {
-        rc = launch_few_up<4, 2, 8, false>(p, 2, s);
-        return rc != MOE_OK ? rc : launch_few_down<4, 2, 8>(p, s);
+        rc = launch_few_up<4, 2, 4, false>(p, 4, s);
+        return rc != MOE_OK ? rc : launch_few_down<4, 2, 4>(p, s);
     }
     if (rows >= 8 && p.T > 16) {
-        rc = launch_few_up<2, 2, 8, false>(p, 2, s);
-        return rc != MOE_OK ? rc : launch_few_down<2, 2, 8>(p, s);
-    }
-    if (rows >= 8) {
-        rc = launch_few_up<1, 3, 8, false>(p, 2, s);
-        return rc != MOE_OK ? rc : launch_few_down<1, 3, 8>(p, s);
+        rc = launch_few_up<2, 2, 4, false>(p, 4, s);
+        return rc != MOE_OK ? rc : launch_few_down<2, 2, 4>(p, s);
     }
     const double active = p.e_local * (1.0 - pow(1.0 - (double)p.K / p.E, p.T));
     const double blocks = active * ((p.F + 127) / 128);
-    const bool wide = (blocks >= 0.4 * cus && blocks <= 1.03 * cus) || blocks >= 1.7 * cus;
+    const bool wide = rows < 8 && ((blocks >= 0.4 * cus && blocks <= 1.03 * cus) || blocks >= 1.7 * cus);
     if (wide) rc = p.T > 32 ? launch_few_up<1, 4, 8, true>(p, 1, s) : launch_few_up<1, 2, 8, true>(p, 2, s);
-    else if (p.T > 32) rc = launch_few_up<1, 3, 8, false>(p, 2, s);
-    else if (std::min(p.e_local, p.T * p.K) * (p.F / 64) <= cus) rc = launch_few_up<1, 3, 4, false>(p, 3, s);
+    else if (rows >= 8 || p.T > 32 || std::min(p.e_local, p.T * p.K) * (p.F / 64) <= cus)
+        rc = launch_few_up<1, 3, 4, false>(p, 3, s);
     else rc = launch_few_up<1, 2, 4, false>(p, 4, s);
     return rc != MOE_OK ? rc : launch_few_down<1, 3, 4>(p, s);
 }
@@ -456,6 +463,7 @@ extern "C" int moe_layer_few(const float* logits, const moe_bf16* x, int T, int 
     p.active = (FewExpert*)(b + z.active);
     p.pos = (int*)(b + z.pos);
     p.h = (uint16_t*)(b + z.h);
+    p.h_rest = (uint32_t)(T * std::min(K, e_local) * F * 2);
     p.y = (float*)(b + z.y);
     return launch_few(p, (hipStream_t)stream);
 }

@@ -33,13 +33,16 @@ struct ColumnPiece<8> {
 
 // MATS matrices of one shape, MT tiles of 16 rows, S stages (a stage: 32
 // contraction values) of which S - 1 are in flight.  NTL: the weights carry the
-// non-temporal hint.
-template <int MATS, int CW, int MT, int S, bool NTL>
+// non-temporal hint.  PAIR: a row is the sum of two bf16 rows (its rounded values and
+// what the rounding left), the second `rest` bytes behind the first; the weights'
+// operands serve both.
+template <int MATS, int CW, int MT, int S, bool NTL, bool PAIR = false>
 struct RowStream {
+    static constexpr int kParts = PAIR ? 2 : 1;
     typedef typename ColumnPiece<CW>::type piece;
     struct Stage {
         piece w[MATS][8];
-        u32x4 x[MT];
+        u32x4 x[kParts][MT];
     };
     f32x4 acc[MATS][CW][MT];
 
@@ -47,7 +50,8 @@ struct RowStream {
     // x_at[m]: byte offset in x of row 16*m + l%16 (or of any valid row); rows: how many there are.
     // Contraction steps first, first + step, ... below end, 32 values each.
     __device__ __forceinline__ void run(const uint16_t* const (&w)[MATS], int ld, int col, const uint16_t* x,
-                                        const uint32_t (&x_at)[MT], int rows, int first, int step, int end) {
+                                        const uint32_t (&x_at)[MT], int rows, int first, int step, int end,
+                                        uint32_t rest = 0) {
         const int g = (threadIdx.x & 63) >> 4;
         const uint32_t w_at = ((uint32_t)(8 * g) * (uint32_t)ld + (uint32_t)col) * 2u;
         Stage st[S];
@@ -67,8 +71,11 @@ struct RowStream {
                     s.w[q][i] = NTL ? __builtin_nontemporal_load(p) : *p;
                 }
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-                if (m == 0 || 16 * m < rows) s.x[m] = *(const u32x4*)((const char*)x + x_at[m] + (uint32_t)(kt * 64 + 16 * g));
+            for (int h = 0; h < kParts; ++h)
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    if (m == 0 || 16 * m < rows)
+                        s.x[h][m] = *(const u32x4*)((const char*)x + x_at[m] + ((uint32_t)(kt * 64 + 16 * g) + h * rest));
         };
         auto multiply = [&](const Stage& s) {
 #pragma unroll
@@ -81,10 +88,13 @@ struct RowStream {
                         v[i] = __builtin_amdgcn_perm(s.w[q][2 * i + 1][t >> 1], s.w[q][2 * i][t >> 1],
                                                      t & 1 ? 0x07060302u : 0x05040100u);
 #pragma unroll
-                    for (int m = 0; m < MT; ++m)
-                        if (m == 0 || 16 * m < rows)
-                            acc[q][t][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                __builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, s.x[m]), acc[q][t][m], 0, 0, 0);
+                    for (int h = 0; h < kParts; ++h)
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+                            if (m == 0 || 16 * m < rows)
+                                acc[q][t][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                    __builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, s.x[h][m]), acc[q][t][m], 0, 0,
+                                    0);
                 }
         };
 #pragma unroll
@@ -109,8 +119,8 @@ struct WaveSums {
     static constexpr int kPitch = kCols + 4;
     float v[W][16][kPitch];
 
-    template <int MT, int S, bool NTL>
-    __device__ __forceinline__ void put(const RowStream<MATS, CW, MT, S, NTL>& r, int m, int wave, int lane) {
+    template <int MT, int S, bool NTL, bool PAIR>
+    __device__ __forceinline__ void put(const RowStream<MATS, CW, MT, S, NTL, PAIR>& r, int m, int wave, int lane) {
         const int row = lane & 15, g = lane >> 4;
 #pragma unroll
         for (int q = 0; q < MATS; ++q)

@@ -125,6 +125,35 @@ def test_tokens_without_a_local_expert(EL, with_residual):
         assert ((out.double() - want).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("H,F,E,K", [(256, 256, 128, 8), (320, 192, 16, 4), (128, 128, 8, 8), (192, 2048, 64, 2)])
+def test_bits_in_every_form(H, F, E, K):
+    """A token alone, and among as many others as each form of the kernels takes: the same bits."""
+    logits, x, wg, wu, wd = layer(23, 64, H, F, E, E)
+    out = _lib.moe_layer_few(logits, x, K, 0, wg, wu, wd)[0]
+    for T in (1, 2, 5, 15, 16, 17, 31, 32, 33, 48, 63):
+        print(f"[few] forms T={T} H={H} F={F} E={E} K={K}", flush=True)
+        got = _lib.moe_layer_few(logits[:T].contiguous(), x[:T].contiguous(), K, 0, wg, wu, wd)[0]
+        assert torch.equal(got, out[:T])
+
+
+def test_large_values_between_the_products():
+    """h past the largest bf16 is an infinity there, as one rounding makes it, and no NaN."""
+    T, H, F = 3, 64, 64
+    logits = torch.zeros((T, 1), device="cuda")
+    x = torch.zeros((T, H), dtype=BF, device="cuda")
+    x[:, 0] = 1
+    wg, wu = (torch.zeros((1, H, F), dtype=BF, device="cuda") for _ in range(2))
+    wd = torch.zeros((1, F, H), dtype=BF, device="cuda")
+    wg[:, 0], wu[:, 0, :] = 2.0 ** 64, 2.0 ** 62  # silu(2^64) * 2^62 = 2^126
+    wd[0, 0] = 1.0
+    out = _lib.moe_layer_few(logits, x, 1, 0, wg, wu, wd)[0]
+    assert torch.equal(out, torch.full_like(out, 2.0 ** 126))
+    wu[:, 0, :] = 2.0 ** 64
+    wd[:] = 1.0
+    out = _lib.moe_layer_few(logits, x, 1, 0, wg, wu, wd)[0]
+    assert torch.isinf(out).all() and (out > 0).all()
+
+
 def test_ties_go_to_the_lowest_expert():
     T, E, K = 9, 200, 5
     logits, x, wg, wu, wd = layer(11, T, 64, 64, E, E)
