@@ -326,34 +326,12 @@ __global__ __launch_bounds__(back_threads(G)) void norm_backward_kernel(
     }
 }
 
-// 16 columns (4 lanes x 4) by 64 strands of the rows; the strands' sums meet in LDS, sixteen threads add four
-// neighbouring strands each and one adds the sixteen, in order.
 __global__ __launch_bounds__(256) void column_sums_kernel(const float* __restrict__ part, int rows, int64_t stride, int n,
                                                           float* __restrict__ out0, float* __restrict__ out1) {
-    __shared__ f32x4 s_sum[64][4];
-    const int lane = threadIdx.x & 3, strand = threadIdx.x >> 2;
     // the blocks of out0's columns, then those of out1's
     const bool second = !out0 || (int)blockIdx.x * 16 >= n;
-    const int c = (int)blockIdx.x * 16 + lane * 4 - (second && out0 ? n : 0);
-    const float* at = part + (second ? n : 0) + c;
-    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int p = strand; p < rows; p += 64) acc += *(const f32x4*)(at + p * stride);
-    s_sum[strand][lane] = acc;
-    __syncthreads();
-    if (strand < 16) {
-        acc = s_sum[4 * strand][lane];
-#pragma unroll
-        for (int i = 1; i < 4; ++i) acc += s_sum[4 * strand + i][lane];
-    }
-    __syncthreads();
-    if (strand < 16) s_sum[strand][lane] = acc;
-    __syncthreads();
-    if (strand == 0) {
-#pragma unroll
-        for (int i = 1; i < 16; ++i) acc += s_sum[i][lane];
-        *(f32x4*)((second ? out1 : out0) + c) = acc;
-    }
+    const int c = (int)blockIdx.x * 16 - (second && out0 ? n : 0);
+    sum_columns(part + (second ? n : 0) + c, rows, stride, (second ? out1 : out0) + c);
 }
 
 // Threads of a row and chunks of 8 columns of a thread (G threads hold 8*G*V columns), and the hint, from the sizes.
