@@ -208,7 +208,8 @@ static void plan_rows(LinearPlan& r, int T, int kt, int N) {
     r.form = FORM_ROWS;
     r.wide = T > 32 && N >= 4096;
     const int cols = r.wide ? 128 : 64;
-    const int64_t blocks = (int64_t)((N + cols - 1) / cols) * ((T + 63) / 64);
+    // the backward of no rows asks for a plan too
+    const int64_t blocks = (int64_t)((N + cols - 1) / cols) * std::max(1, (T + 63) / 64);
     int64_t want = 1;
     if (!(T <= 16 && kt <= 64) && 5 * blocks < 4 * cus)
         want = std::max<int64_t>(1, std::min<int64_t>(cus / blocks, kt / 8));
