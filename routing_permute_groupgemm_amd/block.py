@@ -39,7 +39,7 @@ class BlockBuffers:
     pos: torch.Tensor | None = None
     dy: torch.Tensor | None = None
     dab: torch.Tensor | None = None
-    grads: dict | None = None
+    grads: dict | None = None  # buffers of every gradient; backward returns those that there are
 
     @classmethod
     def allocate(cls, shape: MoeShape, shared=0, device="cuda", backward=None, few=False, x_dtype=torch.bfloat16):
@@ -103,8 +103,8 @@ def forward(b: BlockBuffers, p: dict, x: torch.Tensor, add: torch.Tensor | None 
 
 
 def backward(b: BlockBuffers, p: dict, d_out: torch.Tensor, d_s: torch.Tensor | None = None):
-    """From the gradients of the forward's out (bf16) and of its s past this block (x's type) -> b.grads: x (add's
-    gradient is the same) and the weights'.  The gates' gradients reach the router."""
+    """From the gradients of the forward's out (bf16) and of its s past this block (x's type) -> the gradients of x (add's
+    is the same) and of the weights that p has, in b.grads' buffers.  The gates' gradients reach the router."""
     if b.grads is None:
         raise _lib.MoeError("backward: these buffers were allocated without one")
     if b.s is None:
@@ -123,4 +123,4 @@ def backward(b: BlockBuffers, p: dict, d_out: torch.Tensor, d_s: torch.Tensor | 
     _lib.moe_combine(b.parts, b.pos, None, out=b.dy)
     _lib.moe_layer_norm_backward(b.dy, b.s, p["norm_weight"], None if rms else b.mean, b.rstd, d_sum=d_s, rms=rms,
                                  dx=g["x"], dw=g["norm_weight"], db=None if rms else g["norm_bias"], ws=b.ws)
-    return g
+    return {k: v for k, v in g.items() if k == "x" or p.get(k) is not None}
