@@ -374,6 +374,18 @@ int moe_router_backward(const moe_bf16* x, int T, int H, const moe_bf16* w_r, in
                         size_t ws_bytes, moe_stream stream);
 
 /*
+ * Gradient of the router's bias: dbias[e] = sum_t dlogits[t,e]   fp32 [E]
+ * from the unrounded score gradient fp32 [T,E], in fp32, in an order that the
+ * sizes and the GPU's number of CUs decide.  T = 0 writes zeros.  E a multiple
+ * of 64 (MOE_ESHAPE), E <= 4096.  ws: device workspace of at least
+ * moe_router_bias_backward_workspace_size(T, E) bytes (may be NULL when that is
+ * 0), one for each of calls that may overlap.
+ */
+size_t moe_router_bias_backward_workspace_size(int T, int E);
+int moe_router_bias_backward(const float* dlogits, int T, int E, float* dbias, void* ws, size_t ws_bytes,
+                             moe_stream stream);
+
+/*
  * Block-scaled storage: what an expert keeps between two uses, in OCP
  * microscaling blocks of 32 values that share one power-of-two scale byte s
  * (s = 255: the block held a NaN or an infinity and stands for 32 NaN).

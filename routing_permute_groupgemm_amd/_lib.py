@@ -48,6 +48,8 @@ SIGNATURES = {
     "moe_router_workspace_size": ([_i, _i, _i], _z),
     "moe_router_logits": ([_p, _i, _i, _p, _i, _p, _p, _p, _z, _p], _i),
     "moe_router_backward": ([_p, _i, _i, _p, _i, _p, _p, _p, _p, _z, _p], _i),
+    "moe_router_bias_backward_workspace_size": ([_i, _i], _z),
+    "moe_router_bias_backward": ([_p, _i, _i, _p, _p, _z, _p], _i),
     "moe_pack8": ([_p, _i64, _i, _p, _i, _p, _p, _p], _i),
     "moe_unpack8": ([_p, _p, _i64, _i, _p, _i, _p, _p], _i),
     "moe_grouped_gemm_swiglu_save8": ([_p, _p, _p, _p, _i, _i, _i, _i, _p, _p, _p, _p], _i),
@@ -952,6 +954,22 @@ def moe_layer_norm_backward(dy, s, weight, mean, rstd, d_sum=None, rms=False, wa
     _check(lib.moe_layer_norm_backward(_ptr(dy), _ptr(s), f32, T, H, w, m, r, int(rms), d, _ptr(dx), _ptr(dw),
                                        _ptr(db), _ptr(ws), size, _handle(stream, dev)))
     return dx, dw, db
+
+
+def moe_router_bias_backward_workspace_size(T, E) -> int:
+    return int(load().moe_router_bias_backward_workspace_size(T, E))
+
+
+def moe_router_bias_backward(dlogits, dbias=None, ws=None, stream=None):
+    """-> dbias fp32 [E], the gradient of moe_router_logits' bias: the column sums of dlogits fp32 [T, E]."""
+    dev = _device(stream, dlogits)
+    _arg(dlogits, torch.float32, "dlogits", dev)
+    T, E = _rank2(dlogits, "dlogits")
+    dbias = _like(dbias, (E,), torch.float32, "dbias", dev, stream, dlogits)
+    lib = load()
+    ws, size = _ws(ws, lib.moe_router_bias_backward_workspace_size(T, E), dev, stream)
+    _check(lib.moe_router_bias_backward(_ptr(dlogits), T, E, _ptr(dbias), _ptr(ws), size, _handle(stream, dev)))
+    return dbias
 
 
 def _act(act):

@@ -55,6 +55,7 @@ class BlockBuffers:
             need.append(_lib.moe_linear_workspace_size(T, shared, H))
         if backward:
             need.append(_lib.moe_layer_norm_backward_workspace_size(T, H))
+            need.append(_lib.moe_router_bias_backward_workspace_size(T, E))
             if shared:
                 need.append(_lib.moe_linear_backward_workspace_size(T, shared, H))
         layer = (pipeline.FewBuffers.allocate(shape, device) if few else
@@ -76,7 +77,7 @@ class BlockBuffers:
             b.dab = e((T, 2 * shared)) if shared else None
             f32 = lambda *s: e(s, dt=torch.float32)  # noqa: E731
             b.grads = {"x": e((T, H), dt=x_dtype), "norm_weight": f32(H), "norm_bias": f32(H), "w_r": f32(H, E),
-                       "w_gate": layer.dw_gate, "w_up": layer.dw_up, "w_down": layer.dw_down}
+                       "router_bias": f32(E), "w_gate": layer.dw_gate, "w_up": layer.dw_up, "w_down": layer.dw_down}
             if shared:
                 b.grads.update(shared_gate=f32(1, H, shared), shared_up=f32(1, H, shared), shared_down=f32(1, shared, H))
         return b
@@ -113,6 +114,8 @@ def backward(b: BlockBuffers, p: dict, d_out: torch.Tensor, d_s: torch.Tensor | 
     rms = p.get("norm_bias") is None
     pipeline.backward(b.layer, {"d_out": d_out, "x": b.y, "w_gate": p["w_gate"], "w_up": p["w_up"], "w_down": p["w_down"]})
     _lib.moe_router_backward(b.y, p["w_r"], b.layer.dlogits, dx=b.parts[T:2 * T], dw_r=g["w_r"], ws=b.ws)
+    if p.get("router_bias") is not None:
+        _lib.moe_router_bias_backward(b.layer.dlogits, dbias=g["router_bias"], ws=b.ws)
     if Fs:
         _lib.moe_grouped_gemm(d_out, p["shared_down"], None, 1, b.one, H, Fs, T, b.dab,
                               epilogue=_lib.MOE_EPI_SWIGLU_BWD, ab=b.ab)

@@ -3,6 +3,8 @@ the host."""
 import pytest
 
 from routing_permute_groupgemm_amd import _lib, block, synth
+from test_block_calls_cpu import EALIGN, EINVAL, ESHAPE, EWORKSPACE, FAKE, MIS, caller
+from test_stream_argument_cpu import F32, Traced, check, z
 
 
 @pytest.mark.parametrize("Kd,N", [(64, 64), (2048, 64), (2112, 64), (7168, 2048), (2048, 7168), (1 << 21, 64)])
@@ -16,3 +18,19 @@ def test_block_of_no_tokens_is_allocated():
     shape = synth.WORKLOADS["tiny"].scaled(T=0, H=192, F=128, E=64, K=3, backward=True)
     b = block.BlockBuffers.allocate(shape, shared=2112, device="cpu")
     assert b.out.shape == (0, 192) and b.grads["shared_down"].shape == (1, 2112, 192)
+
+
+def test_router_bias_backward_rejects():
+    size = _lib.load().moe_router_bias_backward_workspace_size
+    need = size(300, 128)
+    assert need > 0 and size(0, 128) == size(32, 128) == size(-1, 128) == size(300, 96) == size(300, 4160) == 0
+    call = caller("moe_router_bias_backward", dlogits=FAKE, T=300, E=128, dbias=FAKE, ws=FAKE, ws_bytes=need)
+    for kw, want in ((dict(T=-1), EINVAL), (dict(E=0), EINVAL), (dict(E=4160), EINVAL), (dict(E=96), ESHAPE),
+                     (dict(dlogits=None), EINVAL), (dict(dbias=None), EINVAL), (dict(dlogits=MIS), EALIGN),
+                     (dict(dbias=MIS), EALIGN), (dict(ws=MIS), EALIGN), (dict(ws=None), EWORKSPACE),
+                     (dict(ws_bytes=need - 1), EWORKSPACE)):
+        assert call(**kw) == want, kw
+
+
+def test_buffers_of_the_router_bias_gradient_with_a_stream(monkeypatch):
+    check(Traced(monkeypatch), lambda s: _lib.moe_router_bias_backward(z(4, 64, dtype=F32), stream=s))
