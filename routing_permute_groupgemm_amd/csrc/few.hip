@@ -275,21 +275,13 @@ __device__ __forceinline__ void combine_few(const FewParams& p, int col0) {
     }
 }
 
-template <int MT, int S, int W, bool NTL>
-__global__ __launch_bounds__(64 * W) void few_down(FewParams p) {
-    __shared__ __attribute__((aligned(16))) WaveSums<1, 8, W> sums;
-    __shared__ int s_last;
+// A pass over the rows of expert e and the columns col0 .. col0+127 of its down product, into p.y; PAIR: both values of h.
+// Of a pass without the second, the sums that the pass with both left finite stay.  Whether a sum was not finite -> far.
+template <int MT, int S, int W, bool NTL, bool PAIR>
+__device__ __forceinline__ void down_rows(const FewParams& p, const FewExpert& e, int col0, WaveSums<1, 8, W>& sums,
+                                          bool& far) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int slabs = (p.H + kFewDownCols - 1) / kFewDownCols;
-    const int n_active = *p.n_active;
-    const int a = (int)blockIdx.x / slabs, slab = (int)blockIdx.x - a * slabs, col0 = slab * kFewDownCols;
-    if (a >= n_active) {
-        // no pair is local: the sums are empty
-        if (n_active == 0 && a == 0) combine_few<W>(p, col0);
-        return;
-    }
-    const FewExpert e = p.active[a];
     const int j = __builtin_amdgcn_readfirstlane(e.j);
     const int end = __builtin_amdgcn_readfirstlane(e.row0 + e.rows);
     const uint16_t* const w[1] = {p.w_down + (int64_t)j * p.F * p.H};
@@ -299,7 +291,7 @@ __global__ __launch_bounds__(64 * W) void few_down(FewParams p) {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
             x_at[m] = (uint32_t)(row0 + min(16 * m + (lane & 15), rows - 1)) * (uint32_t)(p.F * 2);
-        RowStream<1, 8, MT, S, NTL, true> r;
+        RowStream<1, 8, MT, S, NTL, PAIR> r;
         // columns past the last are read as the last ones; their sums are not stored
         r.run(w, p.H, min(col0 + 8 * (lane & 15), p.H - 8), p.h, x_at, rows, wave, W, p.F / 32, p.h_rest);
 #pragma unroll
@@ -310,16 +302,53 @@ __global__ __launch_bounds__(64 * W) void few_down(FewParams p) {
             __syncthreads();
             for (int i = tid; i < 512; i += 64 * W) {
                 const int row = i >> 5, c = (i & 31) * 4;
-                if (16 * m + row < rows && col0 + c < p.H)
-                    store_shared(p.y + (int64_t)(row0 + 16 * m + row) * p.H + col0 + c, sums.get(row, c));
+                if (16 * m + row >= rows || col0 + c >= p.H) continue;
+                float* at = p.y + (int64_t)(row0 + 16 * m + row) * p.H + col0 + c;
+                f32x4 v = sums.get(row, c);
+                if constexpr (PAIR) {
+                    far |= !(fabsf(v[0]) + fabsf(v[1]) + fabsf(v[2]) + fabsf(v[3]) < __builtin_inff());
+                } else {
+                    const f32x4 u = load_shared(at);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = fabsf(u[k]) < __builtin_inff() ? u[k] : v[k];
+                }
+                store_shared(at, v);
             }
         }
     }
+}
+
+template <int MT, int S, int W, bool NTL>
+__global__ __launch_bounds__(64 * W) void few_down(FewParams p) {
+    __shared__ __attribute__((aligned(16))) WaveSums<1, 8, W> sums;
+    __shared__ int s_last, s_far;
+    const int tid = threadIdx.x;
+    const int slabs = (p.H + kFewDownCols - 1) / kFewDownCols;
+    const int n_active = *p.n_active;
+    const int a = (int)blockIdx.x / slabs, slab = (int)blockIdx.x - a * slabs, col0 = slab * kFewDownCols;
+    if (a >= n_active) {
+        // no pair is local: the sums are empty
+        if (n_active == 0 && a == 0) combine_few<W>(p, col0);
+        return;
+    }
+    if (tid == 0) s_far = 0;  // an expert has a row, and its pass a barrier before the flag is set
+    const FewExpert e = p.active[a];
+    bool far = false;
+    down_rows<MT, S, W, NTL, true>(p, e, col0, sums, far);
+    if (far) s_far = 1;
     // The last of the column block's workgroups to count itself finds every other's rows in memory: a wave's stores
     // have arrived there when its count of outstanding ones is 0, all waves have when the barrier is passed, and only
     // then does the workgroup count itself.  The last one's loads are issued after it has the full count.
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
+    // An infinite weight times a rest that is 0 or of the other sign is a NaN where the product with h is an infinity:
+    // sums that are not finite are taken again from the rounded values alone.  Looking for them costs what a barrier's flag
+    // does (64 tokens on the sizes B and C below: 237 us without and 240 with it, 446 to 451 and 446 to 453).
+    if (s_far) {
+        down_rows<MT, S, W, NTL, false>(p, e, col0, sums, far);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+    }
     if (tid == 0) s_last = __hip_atomic_fetch_add(p.arrived + slab, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == n_active - 1;
     __syncthreads();
     if (s_last) combine_few<W>(p, col0);
