@@ -34,3 +34,12 @@ def test_router_bias_backward_rejects():
 
 def test_buffers_of_the_router_bias_gradient_with_a_stream(monkeypatch):
     check(Traced(monkeypatch), lambda s: _lib.moe_router_bias_backward(z(4, 64, dtype=F32), stream=s))
+
+
+@pytest.mark.parametrize("T,K,EL,H,F", [(1, 1, 1, 64, 64), (64, 8, 32, 7168, 2048), (64, 8, 2, 7168, 2048),
+                                        (64, 16, 512, 64, 65536), (23, 8, 128, 2048, 768)])
+def test_few_workspace_holds_both_values_of_h(T, K, EL, H, F):
+    """Of every pair that can be local: h in two bf16 values, and the expert's row in fp32."""
+    rows = T * min(K, EL)
+    size = _lib.moe_layer_few_workspace_size(T, K, EL, H, F)
+    assert rows * (4 * F + 4 * H) <= size <= rows * (4 * F + 4 * H) + (1 << 16)

@@ -55,3 +55,36 @@ def test_infinite_weights_and_an_h_that_one_value_holds():
     wd[0, 4, :32] = float("inf")
     out = _lib.moe_layer_few(logits, x, 1, 0, wg, wu, wd)[0]
     assert torch.isposinf(out[:, :32]).all() and (out[:, 32:] == 0).all()
+
+
+def rows_of(h, gates, idx, wd):
+    """Gated sums of the experts' rows from h [E, T, F], and of their magnitudes."""
+    out, mag = (torch.zeros(h.shape[1], wd.shape[2], dtype=torch.float64, device="cuda") for _ in range(2))
+    for j in range(wd.shape[0]):
+        g = (gates * (idx == j)).sum(1, keepdim=True)
+        out += g * (h[j] @ wd[j].double())
+        mag += g * (h[j].abs() @ wd[j].double().abs())
+    return out, mag
+
+
+@pytest.mark.parametrize("T,E,K", FORMS)
+@pytest.mark.parametrize("H,F", [(64, 128), (192, 320)])
+def test_h_keeps_sixteen_bits(T, E, K, H, F):
+    """Every token has one 1, so that gate and up are single weights, without a sum's roundings: h is off by its sigmoid
+    (2^-18), a product and the rounding of its second value (2^-8 of 2^-8); the down product's fp32 sums of 2F products and
+    of K gated rows add theirs, the output rounds once.  An h that is rounded to one bf16 fails the same tolerance, by the
+    outputs that cancel."""
+    logits, _, wg, wu, wd = layer(81 + T, T, H, F, E, E, std=1.0)
+    x = torch.zeros((T, H), dtype=BF, device="cuda")
+    x[torch.arange(T), torch.arange(T) * 7 % H] = 1.0
+    print(f"[few] two values T={T} E={E} K={K} H={H} F={F}", flush=True)
+    out, idx, gates = _lib.moe_layer_few(logits, x, K, 0, wg, wu, wd)
+    g64 = torch.softmax(logits.double().gather(1, idx.long()), 1)
+    h = torch.stack([silu_up(x, wg[j], wu[j]) for j in range(E)])
+    want, mag = rows_of(h, g64, idx, wd)
+    tol = (2.0 ** -16 + 2 * 2.0 ** -18 + (2 * F + K + 4) * 2.0 ** -24) * mag
+    tol = tol + 2.0 ** -8 * (want.abs() + tol) + 1e-37
+    err = (out.double() - want).abs()
+    assert (err <= tol).all(), float((err / tol).max())
+    once = rows_of(h.to(BF).double(), g64, idx, wd)[0]
+    assert ((once - want).abs() > tol).any()  # what the tolerance would not let pass
