@@ -43,3 +43,16 @@ def test_few_workspace_holds_both_values_of_h(T, K, EL, H, F):
     rows = T * min(K, EL)
     size = _lib.moe_layer_few_workspace_size(T, K, EL, H, F)
     assert rows * (4 * F + 4 * H) <= size <= rows * (4 * F + 4 * H) + (1 << 16)
+
+
+def test_partial_sums_of_the_dense_product_are_a_few_times_its_operands():
+    """A chunk of a contraction is at least 256 values deep and there are about as many workgroups as CUs, which leaves the
+    partial sums at up to 2.8 times the operands (1000 x 1024 x 1024 backward); none for no rows."""
+    widths = (64, 192, 768, 1024, 2048, 4096, 7168)
+    for Kd in widths:
+        for N in widths:
+            assert _lib.moe_linear_backward_workspace_size(0, Kd, N) == 0
+            for T in (1, 2, 17, 33, 64, 65, 200, 256, 257, 700, 1000, 2000, 4001, 16384, 131072):
+                most = max(4 * 2 * (T * Kd + Kd * N + T * N), 1 << 20)
+                assert _lib.moe_linear_workspace_size(T, Kd, N) <= most, (T, Kd, N)
+                assert _lib.moe_linear_backward_workspace_size(T, Kd, N) <= most, (T, Kd, N)
