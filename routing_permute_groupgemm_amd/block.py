@@ -42,11 +42,16 @@ class BlockBuffers:
     grads: dict | None = None  # buffers of every gradient; backward returns those that there are
 
     @classmethod
-    def allocate(cls, shape: MoeShape, shared=0, device="cuda", backward=None, few=False, x_dtype=torch.bfloat16):
+    def allocate(cls, shape: MoeShape, shared=0, device="cuda", backward=None, few=False, x_dtype=torch.bfloat16,
+                 cap: int | None = None):
         """few: a decode step of at most _lib.MOE_FEW_TOKENS tokens in the few-token form; x_dtype: the residual
-        stream's type, bf16 or fp32."""
+        stream's type, bf16 or fp32; cap: the rows that the experts' buffers hold, as MoeBuffers.allocate's: on a share of
+        the experts twice the expected rows unless it is given, pairs beyond it are dropped and layer.status says so
+        (T * min(K, EL) holds every pair; the few-token form always does)."""
         if few and backward:
             raise _lib.MoeError("allocate: the few-token form is for the forward only")
+        if few and cap is not None:
+            raise _lib.MoeError("allocate: the few-token form has no capacity")
         backward = False if few else shape.backward if backward is None else backward
         T, H, E = shape.T, shape.H, shape.E
         e = lambda *s, dt=torch.bfloat16: torch.empty(*s, dtype=dt, device=device)  # noqa: E731
@@ -59,7 +64,7 @@ class BlockBuffers:
             if shared:
                 need.append(_lib.moe_linear_backward_workspace_size(T, shared, H))
         layer = (pipeline.FewBuffers.allocate(shape, device) if few else
-                 pipeline.MoeBuffers.allocate(shape, device=device, backward=backward))
+                 pipeline.MoeBuffers.allocate(shape, cap=cap, device=device, backward=backward))
         b = cls(shape=shape, shared=shared, layer=layer, y=e((T, H)), mean=e(T, dt=torch.float32),
                 rstd=e(T, dt=torch.float32), logits=e((T, E), dt=torch.float32), ws=e(max(need), dt=torch.uint8),
                 out=e((T, H)) if shared else layer.out, sum=e((T, H), dt=x_dtype))

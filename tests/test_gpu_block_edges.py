@@ -119,3 +119,24 @@ def test_router_bias_backward_at_its_edges():
                dict(dbias=out[:64]), dict(dbias=out.double()), dict(ws=out)):
         with pytest.raises(_lib.MoeError):
             _lib.moe_router_bias_backward(**dict(dict(dlogits=d), **kw))
+
+
+def test_block_on_a_share_that_every_token_chooses():
+    """More rows than twice the expected: dropped and said so at the default capacity; with room for every pair, or in the
+    few-token form, the output of all of them."""
+    T = 6
+    shape = SHAPE.scaled(T=T, e_local=8, e_begin=16, backward=False)
+    p = weights(shape, 64, True)
+    p["router_bias"][16:24] += 50.0
+    x = rand(5, T, 192)
+    ref = {k: v.double() for k, v in p.items()}
+    b = block.BlockBuffers.allocate(shape, shared=64)
+    block.forward(b, p, x)
+    assert b.layer.cap < 3 * T and int(b.layer.status[0]) == 1
+    for kw in (dict(cap=3 * T), dict(few=True)):
+        b = block.BlockBuffers.allocate(shape, shared=64, **kw)
+        s, out = block.forward(b, p, x)
+        assert kw.get("few") or int(b.layer.status[0]) == 0
+        near("out", out, reference(ref, s.double(), None, b.layer.topk_idx.long(), 16)[1], 4)
+    with pytest.raises(_lib.MoeError):
+        block.BlockBuffers.allocate(shape, few=True, cap=3 * T)
