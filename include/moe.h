@@ -515,9 +515,11 @@ int moe_grouped_gemm4_combine(const moe_bf16* a, const uint8_t* q4, const uint8_
  * a decode step on bf16 weights, in two launches.
  *   topk_idx, gates as moe_route writes them (bit for bit);
  *   out[t] = bf16( residual[t] + sum over k ascending, e = topk_idx[t,k] local, of gates[t,k] * (h . w_down[j]) )
- *   h = bf16(silu(x[t] . w_gate[j]) * (x[t] . w_up[j])),   j = e - e_begin
- * with fp32 sums and one rounding of out; a token without a local expert gets
- * its residual, or +0.  A token's bits do not depend on the other tokens' values.
+ *   h = silu(x[t] . w_gate[j]) * (x[t] . w_up[j]),   j = e - e_begin
+ * with fp32 sums and one rounding of out; h is kept as two bf16 values, itself
+ * rounded and what that left (16 bits; past the largest bf16 an infinity).  A
+ * token without a local expert gets its residual, or +0.  A token's bits do not
+ * depend on the other tokens, nor on how many there are.
  *   logits fp32 [T,E];  x bf16 [T,H];  w_gate, w_up bf16 [e_local,H,F];
  *   w_down bf16 [e_local,F,H];  residual bf16 [T,H] or NULL (it may be out);
  *   topk_idx int32 [T,K], gates fp32 [T,K], out bf16 [T,H] out;
@@ -525,9 +527,10 @@ int moe_grouped_gemm4_combine(const moe_bf16* a, const uint8_t* q4, const uint8_
  *   H, F) bytes, which the call initialises itself; one for each of calls that
  *   may overlap (graphs that are replayed at once among them).
  * T <= MOE_FEW_TOKENS, e_begin + e_local <= E, H and F <= 65536 (MOE_EINVAL); other
- * limits and errors as moe_route and moe_grouped_gemm_swiglu.  Every weight of an expert
- * that has a token is read once, so it is the faster form while the tokens are
- * few; pipeline.forward takes any number of them.
+ * limits and errors as moe_route and moe_grouped_gemm_swiglu.  The weights of an expert
+ * are read once for every 16 rows that it has (32 or 64 where the experts have as
+ * many on average), so it is the faster form while the tokens are few;
+ * pipeline.forward takes any number of them.
  */
 #define MOE_FEW_TOKENS 64
 size_t moe_layer_few_workspace_size(int T, int K, int e_local, int H, int F);

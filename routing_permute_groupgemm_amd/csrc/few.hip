@@ -8,8 +8,8 @@
 // only one that counts.  The down product reads so few rows that the second costs nothing beside the weights (H = 4096, F =
 // 1536, 128 experts, 64 tokens 827 us without and 836 with it, 16 tokens 532 and 534), but for experts with dozens of rows
 // (8 experts, 64 rows each: 144 and 155).
-// Almost every byte is a weight of an expert that has a token, read once (6*H*F
-// bytes each): the time is that of streaming them.
+// Almost every byte is a weight of an expert that has a token (6*H*F bytes each), read once for every 16 rows that the
+// expert has (32 or 64 where they have as many on average): the time is that of streaming them.
 //
 //   few_up    every workgroup routes the T tokens itself (T <= 64, so an expert's
 //             tokens are a 64-bit mask and a token's row among them a popcount), then

@@ -163,9 +163,11 @@ __global__ __launch_bounds__(256) void linear_join(const float* __restrict__ db_
     }
 }
 
-// What a product on the GroupGEMM kernel takes, in us, fitted to what it was measured to take on the MI355X (every form
-// and number of chunks, 257 to 65536 rows by 256 to 8192 columns and contraction values: the form that these choose was
-// the fastest or within 10% of it).  A step is 32 contraction values, `step` and `fixed` a step's and a tile's share.
+// What a product on the GroupGEMM kernel takes, in us, fitted to what it was measured to take on the MI355X.  Of 80
+// products of 257 to 65536 rows by 256 to 8192 columns and contraction values, timed in every tile and number of chunks,
+// what these choose was the fastest or within 5% of it for 73, within 10% for 76, and lost up to 19% for the others
+// (512 x 4096 x 4096 40.7, in four chunks 34.3).  A step is 32 contraction values, `step` and `fixed` a step's and a
+// tile's share.
 // Tiles that have a CU to themselves (all but the 128 x 128 ones of four waves, of which a CU takes two):
 static double tiles_us(int64_t n, int64_t steps, double step, double fixed) {
     const int64_t cus = moe_host::num_cus();
@@ -202,7 +204,8 @@ struct LinearPlan {
 // through memory, so products of few rows and a short contraction are not cut (1 x 2048 x 7168: 8.2, and 8.9 in two), nor
 // those that fill most of the GPU (128 x 2048 x 7168: 17.3, and 22.7 in two).  128 columns, whose workgroups read the rows
 // half as often, where the columns are many: 64 x 7168 x 7168 31 against 38; 128 x 4096 x 1536 15.6 against 13.7.
-// 512 x 4096 x 1536 takes 24 in rows and in tiles, 256 x 4096 x 1536 18 in rows and 22 in tiles.
+// 256 x 4096 x 1536 takes 18 in rows and 22 in tiles, 512 x 4096 x 1536 24 in tiles and more in rows; smaller products of
+// more than 256 rows would still be faster in rows (512 x 2048 x 2048 16 against 24, 1000 x 2048 x 768 16 against 20).
 static void plan_rows(LinearPlan& r, int T, int kt, int N) {
     const int64_t cus = moe_host::num_cus();
     r.form = FORM_ROWS;
